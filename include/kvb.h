@@ -382,6 +382,140 @@ kvb_status kvb_paged_compact_blocks(const kvb_paged_cache* cache, const int32_t*
                                     kvb_stream stream);
 
 /* ------------------------------------------------------------------------
+ * kvb_prefill_attn, kvb_prefill_attn_bwd -- retention-gated causal attention
+ * over packed prompts, and its gradients
+ *
+ * [TRIM] 2.1 over whole prompts, as the gate is trained and as a prompt's
+ * tokens attend before they enter a cache. Document n is rows
+ * [cu[n], cu[n+1]) of the packed tensors; i and j count from its first row.
+ * For query head h (kv head g = h / (Hq / Hkv)):
+ *
+ *     s_ij   = scale * (q_i . k_j)
+ *     x_ij   = cap(s_ij) + max(i - j, 0) * log_beta_j
+ *     cap(s) = softcap * tanh(s / softcap)       (s when softcap == 0)
+ *     row i sees the keys j < max(i + 1, prefix_len[n]) of its document
+ *     o_i    = sum_j softmax(x)_ij v_j,   lse_i = ln sum_j exp(x_ij)
+ *
+ * A key at distance 0 has no bias whatever its log_beta; log_beta may be -inf
+ * (beta = 0: the token is seen at distance 0 alone), must not be NaN. Values
+ * of log_beta beyond +-2^60 count as +-2^60.
+ *
+ * Gradients of a loss with d_o = dL/do and d_lse = dL/dlse (NULL: 0), with
+ * p = softmax(x) and delta_i = sum_j p_ij (d_o_i . v_j) - d_lse_i:
+ *     dx_ij        = p_ij (d_o_i . v_j - delta_i)
+ *     d_log_beta_j = sum over rows i, heads of the group: dx_ij max(i - j, 0)
+ *     ds_ij        = dx_ij (1 - tanh^2(s_ij / softcap))
+ *     dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum ds_ij q_i,
+ *     dv_j = sum p_ij d_o_i           (sums over rows and heads of the group)
+ * Every sum has a fixed order: the same inputs give the same bits.
+ *
+ * Layouts (element strides; the innermost dimension d is contiguous):
+ *   q        [T, Hq, d]  bf16, strides q_stride_t, q_stride_h
+ *   k, v     [T, Hkv, d] bf16, strides kv_stride_t, kv_stride_h
+ *   log_beta [T, Hkv] f32, strides lb_stride_t, lb_stride_h (0 allowed);
+ *            NULL: beta = 1, no bias
+ *   cu       [N + 1] int32; prefix_len [N] int32 or NULL (no prefix), taken
+ *            into [0, length]
+ *   o        [T, Hq, d] bf16 contiguous, lse [T, Hq] f32 contiguous (NULL
+ *            allowed for kvb_prefill_attn; the gradients read it)
+ *   d_o [T, Hq, d] bf16, d_lse [T, Hq] f32 (NULL allowed), dq [T, Hq, d] bf16,
+ *   dk, dv [T, Hkv, d] bf16, d_log_beta [T, Hkv] f32 (given exactly when
+ *   log_beta is): contiguous
+ *   workspace: kvb_prefill_attn_bwd_workspace_bytes(T, Hq) bytes, 16-byte
+ *   aligned; no content is read before it is written. Calls that may run at
+ *   the same time need workspaces of their own.
+ * Rows of no document are neither read into a result nor written. A document
+ * may be empty. cu out of order or outside [0, T] sets KVB_DERR_RANGE and
+ * nothing is written.
+ * An infinity or a NaN in a row of q or k reaches the rows that see it, and no
+ * other document. One in v_j may also reach rows i < j of the same document
+ * (their weight for j is 0, and 0 times it is NaN), as in the formula's
+ * products.
+ *
+ * Requirements: d in {64, 128}; Hq / Hkv in {1, 2, 4, 8}; T <= 2^30, N <=
+ * KVB_PREFILL_MAX_DOCS; q, k, v, o and the bf16 gradients 16-byte aligned;
+ * the strides of q, k, v multiples of 8, at least d; scale 0 (for 1/sqrt(d))
+ * or in [2^-20, 2^20]; softcap 0 or in [2^-20, 2^20].
+ * ---------------------------------------------------------------------- */
+#define KVB_PREFILL_MAX_DOCS 65536
+#define KVB_PREFILL_MIN_SCALE (1.0f / (1 << 20))
+
+typedef struct kvb_prefill_args {
+    const uint16_t* q;
+    int64_t q_stride_t, q_stride_h;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t kv_stride_t, kv_stride_h;
+    const float* log_beta;
+    int64_t lb_stride_t, lb_stride_h;
+    const int32_t* cu;
+    const int32_t* prefix_len;
+    int32_t T, N, Hq, Hkv, d;
+    float scale, softcap;
+    uint16_t* o;
+    float* lse;
+} kvb_prefill_args;
+
+typedef struct kvb_prefill_grads {
+    const uint16_t* d_o;
+    const float* d_lse;
+    uint16_t* dq;
+    uint16_t* dk;
+    uint16_t* dv;
+    float* d_log_beta;
+    void* workspace;
+    size_t workspace_bytes;
+} kvb_prefill_grads;
+
+kvb_status kvb_prefill_attn(const kvb_prefill_args* args, kvb_stream stream);
+
+size_t kvb_prefill_attn_bwd_workspace_bytes(int32_t T, int32_t Hq);
+
+/* args: the arguments of the kvb_prefill_attn call, its o and lse filled */
+kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* args, const kvb_prefill_grads* grads, kvb_stream stream);
+
+/* ------------------------------------------------------------------------
+ * kvb_paged_plan, kvb_paged_write -- whole prompts into a paged cache
+ *
+ * kvb_paged_plan gives the tokens of packed prompts their slots: tokens
+ * [cu[b], cu[b+1]) are appended to every kv head of sequence b. It takes
+ * ceil((len + new) / KVB_PAGE_SLOTS) - ceil(len / KVB_PAGE_SLOTS) pages per
+ * (sequence, kv head) off the top of the free stack, in the order (sequence,
+ * kv head, page), so the pages of a plan are deterministic; it writes their
+ * table entries, len += new, *free_count, and
+ *     slot_map[g, token] = page * KVB_PAGE_SLOTS + slot % KVB_PAGE_SLOTS,
+ * the row of the page pool that holds the token's entry of kv head g.
+ * A sequence is served whole or not at all: it is served when the pages wanted
+ * by all sequences up to it fit the free stack, or when it needs no page. An
+ * unserved sequence keeps its table and len, its tokens get slot -1, and
+ * KVB_DERR_PAGES is set. A sequence whose tokens do not fit its table, whose
+ * len is out of range or, with empty_only != 0, that holds slots already while
+ * it has new tokens, is not served either (KVB_DERR_LEN), and wants no pages.
+ * slot_map entries of tokens outside all sequences are left as they were. cu
+ * out of order or outside [0, T] sets KVB_DERR_RANGE: slot_map is set to -1
+ * throughout and the cache is left as it was.
+ *
+ * kvb_paged_write copies the packed rows of K and V, log_beta (given exactly
+ * when the pool has log_beta_pages) and pos of every token with a slot >= 0 to
+ * its row of the pool; a slot of -1 (or below) is skipped, one past the pool
+ * skipped with KVB_DERR_RANGE. No two tokens of one call may name the same slot.
+ *
+ * Layouts: cu [B + 1] int32; slot_map [Hkv, T] int32 contiguous; k, v
+ * [T, Hkv, d] bf16 with strides kv_stride_t, kv_stride_h (multiples of 8, 0
+ * allowed), 16-byte aligned; log_beta [T, Hkv] f32 with its strides; pos [T]
+ * int32. workspace: kvb_paged_plan_workspace_bytes(B, Hkv) bytes, 16-byte
+ * aligned. T <= 2^30.
+ * ---------------------------------------------------------------------- */
+size_t kvb_paged_plan_workspace_bytes(int32_t B, int32_t Hkv);
+
+kvb_status kvb_paged_plan(const kvb_paged_cache* cache, const int32_t* cu, int32_t T, int32_t* slot_map,
+                          int32_t empty_only, void* workspace, size_t workspace_bytes, kvb_stream stream);
+
+kvb_status kvb_paged_write(const kvb_paged_cache* cache, const uint16_t* k, const uint16_t* v, int64_t kv_stride_t,
+                           int64_t kv_stride_h, const float* log_beta, int64_t lb_stride_t, int64_t lb_stride_h,
+                           const int32_t* pos, const int32_t* slot_map, int32_t T, kvb_stream stream);
+
+/* ------------------------------------------------------------------------
  * kvb_asm_lookup_merge -- attention-state-memory lookup and merge
  *
  * [ASM] steps 3-4. For query token n and head h:

@@ -8,7 +8,7 @@ kvb_asm_aggregate call the _grouped entry points, with the table count taken
 from qbar's first dimension). Every step of the path runs in the library's
 CUDA kernels; there is no other implementation.
 
-Modules: cache (BoundedKVCache: the decode step of one layer), asm_build (the
+Modules: cache (BoundedKVCache, PagedKVCache: the decode step of one layer; PagedKVCache.prefill), asm_build (the
 memory's offline build: clustering, aggregation, two-level index), synth
 (seeded synthetic workloads).
 
@@ -33,6 +33,8 @@ __all__ = [
     "decode_workspace", "evict_candidates",
     "PagedPool", "kvb_paged_reset", "kvb_paged_evict_insert", "kvb_paged_decode_attn", "kvb_paged_compact_blocks",
     "kvb_asm_planes_bytes", "kvb_asm_prepare", "kvb_asm_lookup_merge_planes",
+    "kvb_prefill_attn", "kvb_prefill_attn_bwd_workspace_bytes", "kvb_prefill_attn_bwd",
+    "kvb_paged_plan_workspace_bytes", "kvb_paged_plan", "kvb_paged_write",
 ]
 
 
@@ -643,3 +645,193 @@ def kvb_paged_compact_blocks(pool, rm_start, rm_len, *, stream=None) -> None:
         _need(x, torch.int32, name); _contig(x, name)
     _check(_lib.lib().kvb_paged_compact_blocks(_pool(pool), _ptr(rm_start), _ptr(rm_len), _stream(stream)),
            "kvb_paged_compact_blocks")
+
+
+# ----------------------------------------------------------------------------------------------
+# prompts: attention over packed documents, its gradients, and whole prompts into a paged cache
+# ----------------------------------------------------------------------------------------------
+
+def _one_device(tensors):
+    """The device that all of {name: tensor or None} are on (CUDA); ValueError when they differ."""
+    dev = None
+    for name, x in tensors.items():
+        if x is None:
+            continue
+        if not x.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if dev is not None and x.device != dev:
+            raise ValueError(f"{name} is on {x.device}, the other tensors on {dev}")
+        dev = x.device
+    return dev
+
+
+def _launch(device, stream, call, where):
+    """call(stream) with `device` current (the library launches on the current device)."""
+    with torch.cuda.device(device):
+        _check(call(_stream(stream)), where)
+
+
+def _packed_strides(x, T, H, name):
+    """(token, head) strides of a packed [T, H, d] tensor; those of a dimension of size 1 do not matter."""
+    d = x.shape[2]
+    if x.stride(2) != 1:
+        raise ValueError(f"{name}: innermost dim must be contiguous")
+    sh = x.stride(1) if H > 1 else d
+    st = x.stride(0) if T > 1 else H * d
+    return st, sh
+
+
+def _f32_strides(x, T, H):
+    return (x.stride(0) if T > 1 else 0, x.stride(1) if H > 1 else 0)
+
+
+def _prefill_args(q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap):
+    """Checks and marshals the arguments shared by kvb_prefill_attn and kvb_prefill_attn_bwd."""
+    for name, x in (("q", q), ("k", k), ("v", v), ("cu", cu)):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if q.dim() != 3 or k.dim() != 3 or cu.dim() != 1 or cu.numel() < 1:
+        raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d], cu [N + 1]")
+    T, Hq, d = (int(x) for x in q.shape)
+    Hkv, N = int(k.shape[1]), cu.numel() - 1
+    for name, x, shp in (("k", k, (T, Hkv, d)), ("v", v, (T, Hkv, d)), ("log_beta", log_beta, (T, Hkv)),
+                         ("prefix_len", prefix_len, (N,)), ("o", o, (T, Hq, d)), ("lse", lse, (T, Hq))):
+        _shape(x, shp, name)
+    for name, x in (("q", q), ("k", k), ("v", v), ("o", o)):
+        _need(x, torch.bfloat16, name, cuda=False)
+    for name, x in (("log_beta", log_beta), ("lse", lse)):
+        if x is not None:
+            _need(x, torch.float32, name, cuda=False)
+    for name, x in (("cu", cu), ("prefix_len", prefix_len)):
+        if x is not None:
+            _need(x, torch.int32, name, cuda=False); _contig(x, name)
+    _contig(o, "o")
+    if lse is not None:
+        _contig(lse, "lse")
+    qs, ks, vs = (_packed_strides(x, T, H, n) for x, H, n in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v")))
+    if ks != vs:
+        raise ValueError("k and v need equal strides")
+    ls = (0, 0) if log_beta is None else _f32_strides(log_beta, T, Hkv)
+    dev = _one_device(dict(q=q, k=k, v=v, log_beta=log_beta, cu=cu, prefix_len=prefix_len, o=o, lse=lse))
+    return dev, _lib.PrefillArgs(
+        q=q.data_ptr() or None, q_stride_t=qs[0], q_stride_h=qs[1], k=k.data_ptr() or None, v=v.data_ptr() or None, kv_stride_t=ks[0],
+        kv_stride_h=ks[1], log_beta=None if log_beta is None else log_beta.data_ptr(), lb_stride_t=ls[0],
+        lb_stride_h=ls[1], cu=cu.data_ptr(), prefix_len=None if prefix_len is None else prefix_len.data_ptr(),
+        T=T, N=N, Hq=Hq, Hkv=Hkv, d=d, scale=float(scale), softcap=float(softcap), o=o.data_ptr() or None,
+        lse=None if lse is None else lse.data_ptr())
+
+
+def kvb_prefill_attn(q, k, v, log_beta, cu, o, lse=None, *, prefix_len=None, scale: float = 0.0,
+                     softcap: float = 0.0, stream=None) -> None:
+    """Retention-gated causal attention over packed prompts; see kvb_prefill_attn in include/kvb.h.
+
+    q [T, Hq, d] bf16; k, v [T, Hkv, d] bf16 (equal strides); log_beta [T, Hkv] f32 or None
+    (beta = 1); cu [N + 1] int32: document n is rows cu[n] .. cu[n + 1]; o [T, Hq, d] bf16 and lse
+    [T, Hq] f32 (or None) are written at the documents' rows; prefix_len [N] int32 or None: the
+    first tokens of a document that every one of its rows sees; softcap 0 or the tanh cap of the
+    scores; scale 0 for 1/sqrt(d)."""
+    dev, a = _prefill_args(q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap)
+    if a.T == 0 or a.N == 0:
+        return
+    _launch(dev, stream, lambda s: _lib.lib().kvb_prefill_attn(ctypes.byref(a), s), "kvb_prefill_attn")
+
+
+def kvb_prefill_attn_bwd_workspace_bytes(T: int, Hq: int) -> int:
+    return int(_lib.lib().kvb_prefill_attn_bwd_workspace_bytes(T, Hq))
+
+
+def kvb_prefill_attn_bwd(q, k, v, log_beta, cu, o, lse, d_o, d_lse, dq, dk, dv, d_log_beta, workspace, *,
+                         prefix_len=None, scale: float = 0.0, softcap: float = 0.0, stream=None) -> None:
+    """Gradients of kvb_prefill_attn; see kvb_prefill_attn_bwd in include/kvb.h. The arguments of
+    the forward call with its o and lse filled; d_o [T, Hq, d] bf16, d_lse [T, Hq] f32 or None;
+    dq [T, Hq, d], dk, dv [T, Hkv, d] bf16 and d_log_beta [T, Hkv] f32 (exactly when log_beta is
+    given) are written at the documents' rows. workspace: a uint8 CUDA tensor of at least
+    kvb_prefill_attn_bwd_workspace_bytes(T, Hq) bytes."""
+    if lse is None:
+        raise ValueError("the gradients need lse")
+    if (log_beta is None) != (d_log_beta is None):
+        raise ValueError("d_log_beta is needed exactly when log_beta is given")
+    for name, x in (("q", q), ("k", k)):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if x.dim() != 3:
+            raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d]")
+    (T, Hq, d), Hkv = q.shape, k.shape[1]
+    grads = dict(d_o=d_o, d_lse=d_lse, dq=dq, dk=dk, dv=dv, d_log_beta=d_log_beta)
+    for name, shp in (("d_o", (T, Hq, d)), ("d_lse", (T, Hq)), ("dq", (T, Hq, d)), ("dk", (T, Hkv, d)),
+                      ("dv", (T, Hkv, d)), ("d_log_beta", (T, Hkv))):
+        x = grads[name]
+        if x is None and name not in ("d_lse", "d_log_beta"):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        _shape(x, shp, name)
+    for name, x in grads.items():
+        if x is not None:
+            _need(x, torch.float32 if name in ("d_lse", "d_log_beta") else torch.bfloat16, name, cuda=False); _contig(x, name)
+    _need(workspace, torch.uint8, "workspace", cuda=False); _contig(workspace, "workspace")
+    dev, a = _prefill_args(q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap)
+    _one_device(dict(q=q, workspace=workspace, **grads))
+    if a.T == 0 or a.N == 0:
+        return
+    ptr = {name: None if x is None else x.data_ptr() for name, x in grads.items()}
+    g = _lib.PrefillGrads(workspace=workspace.data_ptr(), workspace_bytes=workspace.numel(), **ptr)
+    _launch(dev, stream, lambda s: _lib.lib().kvb_prefill_attn_bwd(ctypes.byref(a), ctypes.byref(g), s),
+            "kvb_prefill_attn_bwd")
+
+
+def _pool_tensors(pool):
+    if not isinstance(pool, PagedPool):
+        raise TypeError("pool must be a PagedPool")
+    return {n: getattr(pool, n) for n in ("k_pages", "v_pages", "log_beta_pages", "pos_pages", "table", "len",
+                                          "free_pages", "free_count")}
+
+
+def kvb_paged_plan_workspace_bytes(B: int, Hkv: int) -> int:
+    return int(_lib.lib().kvb_paged_plan_workspace_bytes(B, Hkv))
+
+
+def kvb_paged_plan(pool, cu, slot_map, workspace, *, empty_only: bool = False, stream=None) -> None:
+    """Pages and slots for the tokens of packed prompts; see kvb_paged_plan in include/kvb.h. cu
+    [B + 1] int32: tokens cu[b] .. cu[b + 1] are appended to every kv head of sequence b; slot_map
+    [Hkv, T] int32 receives the pool rows (-1: not served). workspace: a uint8 CUDA tensor of at
+    least kvb_paged_plan_workspace_bytes(B, Hkv) bytes. empty_only: sequences that hold slots
+    already are not served."""
+    tensors = _pool_tensors(pool)
+    _shape(cu, (pool.B + 1,), "cu")
+    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 2 or slot_map.shape[0] != pool.Hkv:
+        raise ValueError("slot_map must be [Hkv, T]")
+    for name, x in (("cu", cu), ("slot_map", slot_map)):
+        _need(x, torch.int32, name, cuda=False); _contig(x, name)
+    _need(workspace, torch.uint8, "workspace", cuda=False); _contig(workspace, "workspace")
+    dev = _one_device(dict(tensors, cu=cu, slot_map=slot_map, workspace=workspace))
+    _launch(dev, stream, lambda s: _lib.lib().kvb_paged_plan(
+        _pool(pool), _ptr(cu), int(slot_map.shape[1]), _ptr(slot_map), int(bool(empty_only)), _ptr(workspace),
+        workspace.numel(), s), "kvb_paged_plan")
+
+
+def kvb_paged_write(pool, k, v, log_beta, pos, slot_map, *, stream=None) -> None:
+    """The packed rows k, v [T, Hkv, d] bf16 (equal strides), log_beta [T, Hkv] f32 (exactly when the
+    pool holds log betas) and pos [T] int32 into the pool rows that slot_map [Hkv, T] names; see
+    kvb_paged_write in include/kvb.h."""
+    tensors = _pool_tensors(pool)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k and v must be [T, Hkv, d]")
+    T = int(k.shape[0])
+    for name, x, shp in (("k", k, (T, pool.Hkv, pool.d)), ("v", v, (T, pool.Hkv, pool.d)),
+                         ("log_beta", log_beta, (T, pool.Hkv)), ("pos", pos, (T,)), ("slot_map", slot_map, (pool.Hkv, T))):
+        _shape(x, shp, name)
+    if (log_beta is None) != (pool.log_beta_pages is None):
+        raise ValueError("log_beta is needed exactly when the pool holds log betas")
+    for name, x in (("k", k), ("v", v)):
+        _need(x, torch.bfloat16, name, cuda=False)
+    for name, x in (("pos", pos), ("slot_map", slot_map)):
+        _need(x, torch.int32, name, cuda=False); _contig(x, name)
+    if log_beta is not None:
+        _need(log_beta, torch.float32, "log_beta", cuda=False)
+    ks, vs = (_packed_strides(x, T, pool.Hkv, n) for x, n in ((k, "k"), (v, "v")))
+    if ks != vs:
+        raise ValueError("k and v need equal strides")
+    ls = (0, 0) if log_beta is None else _f32_strides(log_beta, T, pool.Hkv)
+    dev = _one_device(dict(tensors, k=k, v=v, log_beta=log_beta, pos=pos, slot_map=slot_map))
+    _launch(dev, stream, lambda s: _lib.lib().kvb_paged_write(
+        _pool(pool), _ptr(k), _ptr(v), ks[0], ks[1], _ptr(log_beta), ls[0], ls[1], _ptr(pos), _ptr(slot_map), T, s),
+        "kvb_paged_write")

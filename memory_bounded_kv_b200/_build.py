@@ -5,13 +5,14 @@ import glob
 import os
 import shutil
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SO = os.path.join(PKG, "libkvb.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=default"]
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=default"]
 
 
 def _nvcc() -> str:
@@ -34,15 +35,26 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile every .cu of csrc/ (one nvcc each, side by side) and link the objects into libkvb.so."""
     if not force and not stale():
         return SO
-    tmp = SO + f".{os.getpid()}.tmp"
-    cmd = [_nvcc(), *ARCH, *FLAGS, "-o", tmp, os.path.join(CSRC, "kvb.cu")]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
-    os.replace(tmp, SO)
+    with tempfile.TemporaryDirectory(dir=PKG, prefix=f".build.{os.getpid()}.") as tmp:
+        units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+        objs = [os.path.join(tmp, os.path.basename(u) + ".o") for u in units]
+        jobs = []
+        for u, o in zip(units, objs):
+            cmd = [_nvcc(), *ARCH, *FLAGS, "-c", "-o", o, u]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+                print(" ".join(cmd))
+            jobs.append((cmd, subprocess.Popen(cmd)))
+        codes = [(cmd, p.wait()) for cmd, p in jobs]
+        for cmd, code in codes:
+            if code:
+                raise subprocess.CalledProcessError(code, cmd)
+        so = os.path.join(tmp, "libkvb.so")
+        subprocess.check_call([_nvcc(), *ARCH, "-shared", "-o", so, *objs])
+        os.replace(so, SO)
     return SO
 
 

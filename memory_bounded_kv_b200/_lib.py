@@ -22,6 +22,8 @@ EXPORTS = (
     "kvb_abi_version", "kvb_test_withhold_next_decode",
     "kvb_paged_reset", "kvb_paged_evict_insert", "kvb_paged_decode_attn", "kvb_paged_compact_blocks",
     "kvb_asm_planes_bytes", "kvb_asm_prepare", "kvb_asm_lookup_merge_planes",
+    "kvb_prefill_attn", "kvb_prefill_attn_bwd_workspace_bytes", "kvb_prefill_attn_bwd",
+    "kvb_paged_plan_workspace_bytes", "kvb_paged_plan", "kvb_paged_write",
 )
 
 KVB_OK, KVB_EINVAL, KVB_ECUDA, KVB_EDEVICE = 0, 1, 2, 3
@@ -56,6 +58,25 @@ class PagedCacheArgs(ctypes.Structure):
         ("table", _P), ("len", _P), ("free_pages", _P), ("free_count", _P),
         ("B", _I32), ("Hkv", _I32), ("d", _I32), ("max_pages", _I32), ("num_pages", _I32),
     ]
+
+
+class PrefillArgs(ctypes.Structure):
+    """Mirror of struct kvb_prefill_args."""
+    _fields_ = [
+        ("q", _P), ("q_stride_t", _I64), ("q_stride_h", _I64),
+        ("k", _P), ("v", _P), ("kv_stride_t", _I64), ("kv_stride_h", _I64),
+        ("log_beta", _P), ("lb_stride_t", _I64), ("lb_stride_h", _I64),
+        ("cu", _P), ("prefix_len", _P),
+        ("T", _I32), ("N", _I32), ("Hq", _I32), ("Hkv", _I32), ("d", _I32),
+        ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+        ("o", _P), ("lse", _P),
+    ]
+
+
+class PrefillGrads(ctypes.Structure):
+    """Mirror of struct kvb_prefill_grads."""
+    _fields_ = [("d_o", _P), ("d_lse", _P), ("dq", _P), ("dk", _P), ("dv", _P), ("d_log_beta", _P),
+                ("workspace", _P), ("workspace_bytes", _SZ)]
 
 
 _lib = None
@@ -111,13 +132,23 @@ def lib() -> ctypes.CDLL:
         L.kvb_asm_planes_bytes.restype = _SZ
         L.kvb_asm_prepare.argtypes = [_P, _I32, _I32, _I32, _P, _SZ, _P]
         L.kvb_asm_lookup_merge_planes.argtypes = [_P, _P, _SZ, _P, _P, _P, _P] + [_I32] * 5 + [_P] * 4 + [_SZ, _P]
+        _PA = ctypes.POINTER(PrefillArgs)
+        L.kvb_prefill_attn.argtypes = [_PA, _P]
+        L.kvb_prefill_attn_bwd_workspace_bytes.argtypes = [_I32, _I32]
+        L.kvb_prefill_attn_bwd_workspace_bytes.restype = _SZ
+        L.kvb_prefill_attn_bwd.argtypes = [_PA, ctypes.POINTER(PrefillGrads), _P]
+        L.kvb_paged_plan_workspace_bytes.argtypes = [_I32, _I32]
+        L.kvb_paged_plan_workspace_bytes.restype = _SZ
+        L.kvb_paged_plan.argtypes = [_PC, _P, _I32, _P, _I32, _P, _SZ, _P]
+        L.kvb_paged_write.argtypes = [_PC, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I32, _P]
         for f in ("kvb_decode_attn", "kvb_decode_attn_noalloc", "kvb_decode_step", "kvb_merge_states", "kvb_evict_insert", "kvb_compact_blocks",
                   "kvb_asm_lookup_merge", "kvb_asm_hier_lookup_merge", "kvb_asm_aggregate",
                   "kvb_asm_entries_bf16", "kvb_asm_index_csr", "kvb_asm_lookup_merge_grouped",
                   "kvb_asm_aggregate_grouped", "kvb_get_error",
                   "kvb_abi_version", "kvb_test_withhold_next_decode", "kvb_paged_reset",
                   "kvb_paged_evict_insert", "kvb_paged_decode_attn", "kvb_paged_compact_blocks",
-                  "kvb_asm_prepare", "kvb_asm_lookup_merge_planes"):
+                  "kvb_asm_prepare", "kvb_asm_lookup_merge_planes", "kvb_prefill_attn",
+                  "kvb_prefill_attn_bwd", "kvb_paged_plan", "kvb_paged_write"):
             getattr(L, f).restype = _I32
         _lib = L
     return _lib

@@ -166,5 +166,28 @@ class PagedKVCache:
         kvb_paged_compact_blocks(self.pool, rm_start, rm_len, stream=stream)
         self.cand_valid = False
 
+    def prefill(self, q, k, v, log_beta, cu, pos, o, lse=None, *, prefix_len=None, softcap=0.0, stream=None):
+        """Whole prompts at once: the packed tokens of sequence b (rows cu[b] .. cu[b + 1] of q
+        [T, Hq, d], k, v [T, Hkv, d], log_beta [T, Hkv], pos [T]) attend among themselves
+        (kvb_prefill_attn, into o and lse) and enter the cache (kvb_paged_plan, kvb_paged_write).
+        A sequence with new tokens must hold none yet; one without keeps what it holds. The pages
+        must have room for the whole prompts; the budget M is enforced by the insertions that
+        follow, each of which replaces a slot of a sequence that holds M or more. kvb_get_error
+        tells of sequences that were not served (their o is written all the same)."""
+        from . import kvb_paged_plan, kvb_paged_plan_workspace_bytes, kvb_paged_write, kvb_prefill_attn
+        if stream is None:
+            stream = torch.cuda.current_stream(self.pool.len.device)
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.pool.len.device)
+        lb = log_beta if self.pool.log_beta_pages is not None else None
+        with torch.cuda.stream(stream):   # the slot map's memory is taken and returned in this stream's order
+            slot_map = torch.full((self.Hkv, k.shape[0]), -1, dtype=torch.int32, device=self.pool.len.device)
+            workspace = torch.empty(kvb_paged_plan_workspace_bytes(self.B, self.Hkv), dtype=torch.uint8,
+                                    device=self.pool.len.device)
+            kvb_prefill_attn(q, k, v, lb, cu, o, lse, prefix_len=prefix_len, softcap=softcap, stream=stream)
+            kvb_paged_plan(self.pool, cu, slot_map, workspace, empty_only=True, stream=stream)
+            kvb_paged_write(self.pool, k, v, lb, pos, slot_map, stream=stream)
+        self.cand_valid = False
+
     def pages_in_use(self) -> int:
         return self.pool.num_pages - int(self.pool.free_count.item())

@@ -17,7 +17,7 @@
 // tf32 would round the centroids and reorder near-ties.
 #pragma once
 
-#include "common.cuh"
+#include "tc5.cuh"
 
 namespace kvb {
 
@@ -79,62 +79,6 @@ constexpr size_t kUB = kUA + kUMT * 2 * kUAHalf;                // [buf][part][k
 constexpr size_t kUBar = kUB + 2 * kUBuf;                       // 2 mbarriers
 constexpr size_t kUSlot = kUBar + 16;                           // tensor-memory base address
 constexpr size_t kUSmem = kUSlot + 16 + 1024;                   // + slack to align the base to 1024
-
-__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4)   // start address
-         | (1ull << 16)                          // leading byte offset (unused for this layout)
-         | (64ull << 32)                         // stride byte offset: 1024 B between 8-row groups
-         | (1ull << 46)                          // descriptor version
-         | (2ull << 61);                         // 128-byte swizzle
-}
-
-// kind::f16 instruction descriptor: f32 accumulator, bf16 A and B, both K-major, M x N
-__host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// hi, mid, lo bf16 pairs of two fp32 values (x0 in the low half of each word)
-__device__ __forceinline__ void split3_bf16x2(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    __nv_bfloat162 t = __floats2bfloat162_rn(x0, x1);
-    hi = *reinterpret_cast<uint32_t*>(&t);
-    const float r0 = x0 - __uint_as_float(hi << 16), r1 = x1 - __uint_as_float(hi & 0xffff0000u);
-    t = __floats2bfloat162_rn(r0, r1);
-    mid = *reinterpret_cast<uint32_t*>(&t);
-    const float s0 = r0 - __uint_as_float(mid << 16), s1 = r1 - __uint_as_float(mid & 0xffff0000u);
-    t = __floats2bfloat162_rn(s0, s1);
-    lo = *reinterpret_cast<uint32_t*>(&t);
-}
 
 // position of one centroid tile in a CTA's stream
 struct AsmTile {

@@ -15,7 +15,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// One error word per GPU; kernels OR bits of enum kvb_device_error into it.
+// One error word per GPU and translation unit; kernels OR bits of enum kvb_device_error into it.
 __device__ unsigned int g_error_word;
 
 __device__ __forceinline__ void raise_error(unsigned bits) { atomicOr(&g_error_word, bits); }

@@ -76,38 +76,6 @@ struct QbtShape {
     static_assert(MISC_OFF >= BAR_OFF + NBAR * 8 && BAR_OFF % 8 == 0, "barriers before the misc words");
 };
 
-// kind::f16 instruction descriptor with an MN-major B operand (bit 16)
-__host__ __device__ constexpr uint32_t umma_idesc_bf16_bmn(int M, int N) { return umma_idesc_bf16(M, N) | (1u << 16); }
-
-// 32 lanes x 16 consecutive columns from registers (lane i of the warp writes lane base + i)
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-// 2^x by the hardware's approximate base-2 exponential (PTX ex2.approx.ftz; 2^-inf = 0)
-__device__ __forceinline__ float ex2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// A bounded wait whose outcome is the same for the whole warp (the warp then runs warp-collective
-// tensor-memory instructions or leaves together).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned long long ns) {
-    return __all_sync(kFull, mbar_wait(bar, parity, ns));
-}
-
-// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle: 64-element MN groups
-// `lbo` bytes apart, 8-row K groups `sbo` bytes apart.
-__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
 template <int G, bool BIAS>
 __global__ void __launch_bounds__(QbtShape<G>::NT, 1)
     decode_attn_qbt_kernel(const __grid_constant__ DecodeQbParams p, const __grid_constant__ CUtensorMap tmK,

@@ -48,7 +48,7 @@
 
 #include <cuda.h>
 
-#include "common.cuh"
+#include "tc5.cuh"
 
 namespace kvb {
 
@@ -131,15 +131,6 @@ static_assert(2 * (TcShape<128, 4>::SMEM + 1024) <= 228 * 1024, "two CTAs per SM
 
 // ---- PTX wrappers -------------------------------------------------------------
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                            uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-        : "memory");
-}
-
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
@@ -179,12 +170,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // 4-byte asynchronous global -> shared copy (cp.async), and the arrival on an mbarrier that happens
 // once every cp.async this thread issued has landed (it counts as one of the barrier's arrivals)
 __device__ __forceinline__ void cp_async4(void* dst_smem, const void* src) {
@@ -215,10 +200,6 @@ __device__ __forceinline__ float ex2_fast(float x) {
 
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // ---- unit bookkeeping shared by producer and consumers --------------------------

@@ -1,0 +1,119 @@
+// libkvb: C ABI (include/kvb.h) of the prompt's path: attention over packed prompts and its
+// gradients, page planning and page writes. As in kvb.cu, the host code validates, picks the
+// kernel and launches it on the caller's stream; it allocates nothing.
+#include <algorithm>
+#include <cmath>
+
+#include "host.cuh"
+#include "paged_fill.cuh"
+#include "prefill_attn.cuh"
+
+kvb_status kvb_prefill_take_error(unsigned* bits) { return take_error_word(bits); }
+
+namespace {
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The host checks of kvb_prefill_attn and its gradients, and the kernels' parameters.
+kvb_status prefill_params(const kvb_prefill_args* a, kvb::PrefillParams* out) {
+    if (a == nullptr) return KVB_EINVAL;
+    if (a->T < 0 || a->T > (1 << 30) || a->N < 0 || a->N > KVB_PREFILL_MAX_DOCS || a->Hq < 1 || a->Hkv < 1) return KVB_EINVAL;
+    if ((a->d != 64 && a->d != 128) || a->Hq % a->Hkv != 0 || a->Hq > 65535) return KVB_EINVAL;
+    const int G = a->Hq / a->Hkv;
+    if (G != 1 && G != 2 && G != 4 && G != 8) return KVB_EINVAL;
+    // the bias rides the score product divided by the scale: both ends keep it in range
+    const double scale = a->scale == 0.0f ? 1.0 / std::sqrt((double)a->d) : (double)a->scale;
+    if (!(scale >= KVB_PREFILL_MIN_SCALE && scale <= 1.0 / KVB_PREFILL_MIN_SCALE)) return KVB_EINVAL;
+    if (a->softcap != 0.0f && !(a->softcap >= KVB_PREFILL_MIN_SCALE && a->softcap <= 1.0f / KVB_PREFILL_MIN_SCALE)) return KVB_EINVAL;
+    if (!a->q || !a->k || !a->v || !a->cu || !a->o) return KVB_EINVAL;
+    if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->o)) return KVB_EINVAL;
+    if (!aligned4(a->log_beta) || !aligned4(a->cu) || !aligned4(a->prefix_len) || !aligned4(a->lse)) return KVB_EINVAL;
+    const long long s[4] = {a->q_stride_t, a->q_stride_h, a->kv_stride_t, a->kv_stride_h};
+    for (long long x : s)
+        if (x < a->d || x % 8 != 0 || x >= (1LL << 38)) return KVB_EINVAL;
+    if (a->log_beta && (a->lb_stride_t < 0 || a->lb_stride_h < 0)) return KVB_EINVAL;
+    kvb::PrefillParams& p = *out;
+    p = kvb::PrefillParams{};
+    p.q = a->q; p.k = a->k; p.v = a->v; p.lb = a->log_beta; p.cu = a->cu; p.prefix = a->prefix_len;
+    p.q_st = a->q_stride_t; p.q_sh = a->q_stride_h; p.kv_st = a->kv_stride_t; p.kv_sh = a->kv_stride_h;
+    p.lb_st = a->lb_stride_t; p.lb_sh = a->lb_stride_h;
+    p.T = a->T; p.N = a->N; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = G;
+    p.scale = (float)scale; p.softcap = a->softcap;
+    p.o = a->o; p.lse = a->lse;
+    return KVB_OK;
+}
+
+template <int D>
+kvb_status launch_rows(const kvb::PrefillParams& p, bool grads, cudaStream_t st) {
+    const dim3 grid(p.N, p.Hq, std::min(64, (p.T + 7) / 8)), kv_grid(p.N, p.Hkv, grid.z);
+    if (!grads) return launch_pdl(kvb::prefill_rows_kernel<D>, grid, dim3(256), 0, st, p);
+    if (launch_pdl(kvb::prefill_dq_rows_kernel<D>, grid, dim3(256), 0, st, p) != KVB_OK) return KVB_ECUDA;
+    return launch_pdl(kvb::prefill_dkv_rows_kernel<D>, kv_grid, dim3(256), 0, st, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+kvb_status kvb_prefill_attn(const kvb_prefill_args* a, kvb_stream stream) {
+    kvb::PrefillParams p;
+    if (prefill_params(a, &p) != KVB_OK) return KVB_EINVAL;
+    if (p.T == 0 || p.N == 0) return KVB_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return a->d == 128 ? launch_rows<128>(p, false, st) : launch_rows<64>(p, false, st);
+}
+
+size_t kvb_prefill_attn_bwd_workspace_bytes(int32_t T, int32_t Hq) {
+    return T < 1 || Hq < 1 ? 0 : (size_t)T * Hq * sizeof(float);
+}
+
+kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* a, const kvb_prefill_grads* g, kvb_stream stream) {
+    kvb::PrefillParams p;
+    if (g == nullptr || prefill_params(a, &p) != KVB_OK) return KVB_EINVAL;
+    if (!a->lse || !g->d_o || !g->dq || !g->dk || !g->dv || (g->d_log_beta != nullptr) != (a->log_beta != nullptr)) return KVB_EINVAL;
+    if (!aligned16(g->d_o) || !aligned16(g->dq) || !aligned16(g->dk) || !aligned16(g->dv)) return KVB_EINVAL;
+    if (!aligned4(g->d_lse) || !aligned4(g->d_log_beta)) return KVB_EINVAL;
+    if (p.T == 0 || p.N == 0) return KVB_OK;
+    if (!g->workspace || !aligned16(g->workspace) ||
+        g->workspace_bytes < kvb_prefill_attn_bwd_workspace_bytes(a->T, a->Hq))
+        return KVB_EINVAL;
+    p.d_o = g->d_o; p.d_lse = g->d_lse; p.dq = g->dq; p.dk = g->dk; p.dv = g->dv; p.dlb = g->d_log_beta;
+    p.delta = static_cast<float*>(g->workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return a->d == 128 ? launch_rows<128>(p, true, st) : launch_rows<64>(p, true, st);
+}
+
+size_t kvb_paged_plan_workspace_bytes(int32_t B, int32_t Hkv) {
+    return B < 1 || Hkv < 1 ? 0 : ((size_t)B * Hkv + 1) * sizeof(int4);
+}
+
+kvb_status kvb_paged_plan(const kvb_paged_cache* c, const int32_t* cu, int32_t T, int32_t* slot_map, int32_t empty_only,
+                          void* workspace, size_t workspace_bytes, kvb_stream stream) {
+    kvb::PagedCache pc;
+    if (paged_view(c, &pc) != KVB_OK) return KVB_EINVAL;
+    if (T < 0 || T > (1 << 30) || !cu || !aligned4(cu) || (T > 0 && !slot_map) || !aligned4(slot_map)) return KVB_EINVAL;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < kvb_paged_plan_workspace_bytes(c->B, c->Hkv)) return KVB_EINVAL;
+    kvb::PagedPlanParams p{pc, cu, slot_map, c->B, T, empty_only, static_cast<int4*>(workspace)};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (launch_pdl(kvb::paged_plan_kernel<1024>, dim3(1), dim3(1024), 0, st, p) != KVB_OK) return KVB_ECUDA;
+    return launch_pdl(kvb::paged_slots_kernel<256>, dim3(c->B * c->Hkv), dim3(256), 0, st, p);
+}
+
+kvb_status kvb_paged_write(const kvb_paged_cache* c, const uint16_t* k, const uint16_t* v, int64_t kv_stride_t,
+                           int64_t kv_stride_h, const float* log_beta, int64_t lb_stride_t, int64_t lb_stride_h,
+                           const int32_t* pos, const int32_t* slot_map, int32_t T, kvb_stream stream) {
+    kvb::PagedCache pc;
+    if (paged_view(c, &pc) != KVB_OK) return KVB_EINVAL;
+    if (T < 0 || T > (1 << 30)) return KVB_EINVAL;
+    if (T == 0) return KVB_OK;
+    if (!k || !v || !pos || !slot_map || !aligned16(k) || !aligned16(v) || !aligned4(pos) || !aligned4(slot_map)) return KVB_EINVAL;
+    if ((c->log_beta_pages != nullptr) != (log_beta != nullptr) || !aligned4(log_beta)) return KVB_EINVAL;
+    if (kv_stride_t < 0 || kv_stride_h < 0 || kv_stride_t % 8 || kv_stride_h % 8 || lb_stride_t < 0 || lb_stride_h < 0)
+        return KVB_EINVAL;
+    kvb::PagedWriteParams p{pc, k, v, log_beta, pos, slot_map, kv_stride_t, kv_stride_h, lb_stride_t, lb_stride_h, T};
+    const long long n = (long long)T * c->Hkv * (c->d / 8);
+    const unsigned grid = (unsigned)std::min<long long>((n + 255) / 256, 148 * 8);
+    return launch_pdl(kvb::paged_write_kernel, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), p);
+}
+
+}  // extern "C"
