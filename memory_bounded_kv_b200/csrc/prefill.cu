@@ -7,6 +7,7 @@
 #include "host.cuh"
 #include "paged_fill.cuh"
 #include "prefill_attn.cuh"
+#include "prefill_fwd.cuh"
 
 kvb_status kvb_prefill_take_error(unsigned* bits) { return take_error_word(bits); }
 
@@ -40,13 +41,55 @@ kvb_status prefill_params(const kvb_prefill_args* a, kvb::PrefillParams* out) {
     p.T = a->T; p.N = a->N; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = G;
     p.scale = (float)scale; p.softcap = a->softcap;
     p.o = a->o; p.lse = a->lse;
+    p.wait_ns = 1000000000ull;
     return KVB_OK;
 }
 
+// Packed rows x [T][H][d] with strides (elements), in boxes of 64 dims x `bh` heads x `bt` tokens (128-byte
+// swizzle; rows past T read zeros).
+bool make_rows_map(CUtensorMap* map, const void* x, int d, int H, int T, long long sh, long long st, int bh, int bt) {
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
+    cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)bh, (cuuint32_t)bt};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The most units of 2^sh tokens that N documents of T tokens in all can have.
+long long most_units(const kvb::PrefillParams& p, int sh) { return ((long long)(p.T >> sh) + p.N) * p.Hkv; }
+
+template <int D, bool BETA, bool CAP>
+kvb_status launch_fwd(const kvb::PrefillParams& p, cudaStream_t st) {
+    using SH = kvb::FwdShape<D>;
+    auto kern = kvb::prefill_fwd_kernel<D, BETA, CAP>;
+    if (set_smem(kern, SH::SMEM) != KVB_OK) return KVB_ECUDA;
+    CUtensorMap mq, mk, mv;
+    if (!make_rows_map(&mq, p.q, D, p.Hq, p.T, p.q_sh, p.q_st, p.G, 128 / p.G) ||
+        !make_rows_map(&mk, p.k, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SH::KT) ||
+        !make_rows_map(&mv, p.v, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SH::KT))
+        return KVB_EINVAL;
+    const int slots = resident_ctas(kern, SH::NT, SH::SMEM);
+    if (slots <= 0) return KVB_ECUDA;
+    int sh = 8;
+    for (int g = p.G; g > 1; g >>= 1) --sh;
+    const int grid = (int)std::min<long long>(slots, most_units(p, sh));
+    return launch_pdl(kern, dim3(grid), dim3(SH::NT), SH::SMEM, st, p, mq, mk, mv);
+}
+
 template <int D>
-kvb_status launch_rows(const kvb::PrefillParams& p, bool grads, cudaStream_t st) {
+kvb_status fwd_dispatch(const kvb::PrefillParams& p, cudaStream_t st) {
+    const bool beta = p.lb != nullptr, cap = p.softcap > 0.f;
+    if (beta) return cap ? launch_fwd<D, true, true>(p, st) : launch_fwd<D, true, false>(p, st);
+    return cap ? launch_fwd<D, false, true>(p, st) : launch_fwd<D, false, false>(p, st);
+}
+
+template <int D>
+kvb_status launch_rows(const kvb::PrefillParams& p, cudaStream_t st) {
     const dim3 grid(p.N, p.Hq, std::min(64, (p.T + 7) / 8)), kv_grid(p.N, p.Hkv, grid.z);
-    if (!grads) return launch_pdl(kvb::prefill_rows_kernel<D>, grid, dim3(256), 0, st, p);
     if (launch_pdl(kvb::prefill_dq_rows_kernel<D>, grid, dim3(256), 0, st, p) != KVB_OK) return KVB_ECUDA;
     return launch_pdl(kvb::prefill_dkv_rows_kernel<D>, kv_grid, dim3(256), 0, st, p);
 }
@@ -60,7 +103,7 @@ kvb_status kvb_prefill_attn(const kvb_prefill_args* a, kvb_stream stream) {
     if (prefill_params(a, &p) != KVB_OK) return KVB_EINVAL;
     if (p.T == 0 || p.N == 0) return KVB_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return a->d == 128 ? launch_rows<128>(p, false, st) : launch_rows<64>(p, false, st);
+    return a->d == 128 ? fwd_dispatch<128>(p, st) : fwd_dispatch<64>(p, st);
 }
 
 size_t kvb_prefill_attn_bwd_workspace_bytes(int32_t T, int32_t Hq) {
@@ -80,7 +123,7 @@ kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* a, const kvb_prefill_gra
     p.d_o = g->d_o; p.d_lse = g->d_lse; p.dq = g->dq; p.dk = g->dk; p.dv = g->dv; p.dlb = g->d_log_beta;
     p.delta = static_cast<float*>(g->workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return a->d == 128 ? launch_rows<128>(p, true, st) : launch_rows<64>(p, true, st);
+    return a->d == 128 ? launch_rows<128>(p, st) : launch_rows<64>(p, st);
 }
 
 size_t kvb_paged_plan_workspace_bytes(int32_t B, int32_t Hkv) {

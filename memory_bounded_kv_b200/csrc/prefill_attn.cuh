@@ -7,40 +7,9 @@
 // has no bias, whatever its log beta (so beta = 0 leaves a token visible to itself alone).
 #pragma once
 
-#include "tc5.cuh"
+#include "prefill_units.cuh"
 
 namespace kvb {
-
-struct PrefillParams {
-    const uint16_t* q;
-    const uint16_t* k;
-    const uint16_t* v;
-    const float* lb;          // log beta or null
-    const int* cu;            // [N + 1]
-    const int* prefix;        // [N] or null
-    long long q_st, q_sh, kv_st, kv_sh, lb_st, lb_sh;   // element strides of a token and of a head
-    int T, N, Hq, Hkv, G;
-    float scale, softcap;     // softcap 0: no cap
-    uint16_t* o;              // [T, Hq, d] bf16
-    float* lse;               // [T, Hq] or null
-    // gradients
-    const uint16_t* d_o;      // [T, Hq, d]
-    const float* d_lse;       // [T, Hq] or null
-    float* delta;             // [T, Hq]: sum_j p_ij (dO_i . v_j) - dlse_i
-    uint16_t* dq;             // [T, Hq, d]
-    uint16_t* dk;             // [T, Hkv, d]
-    uint16_t* dv;             // [T, Hkv, d]
-    float* dlb;               // [T, Hkv] or null
-};
-
-// Whether cu is in order and inside [0, T]; the same for the whole warp. Records KVB_DERR_RANGE if not.
-__device__ __forceinline__ bool prefill_docs_ok(const int* cu, int N, int T) {
-    bool bad = false;
-    for (int n = threadIdx.x & 31; n < N; n += 32) bad |= cu[n] < 0 || cu[n + 1] < cu[n] || cu[n + 1] > T;
-    bad = __any_sync(kFull, bad);
-    if (bad && (threadIdx.x & 31) == 0) raise_error(KVB_DERR_RANGE);
-    return !bad;
-}
 
 // ---- one warp per row: the plainest form -------------------------------------
 
@@ -81,34 +50,7 @@ __device__ __forceinline__ float prefill_logit(const PrefillParams& p, float dot
     return x;
 }
 
-// grid: (documents, kv heads * G, blocks of rows); 8 rows per block step
-template <int D>
-__global__ void __launch_bounds__(256) prefill_rows_kernel(const __grid_constant__ PrefillParams p) {
-    griddep_wait();
-    if (!prefill_docs_ok(p.cu, p.N, p.T)) return;
-    const int s = p.cu[blockIdx.x], e = p.cu[blockIdx.x + 1];
-    const int h = blockIdx.y, g = h / p.G, lane = threadIdx.x & 31, len = e - s;
-    const int pre = prefill_prefix(p, blockIdx.x, len);
-    for (int i = blockIdx.z * 8 + (threadIdx.x >> 5); i < len; i += gridDim.z * 8) {
-        float q[D / 32], o[D / 32] = {}, k[D / 32], v[D / 32];
-        row_load<D>(q, p.q + (long long)(s + i) * p.q_st + h * p.q_sh, lane);
-        float m = -INFINITY, l = 0.f, slope;
-        for (int j = 0; j < max(i + 1, pre); ++j) {
-            row_load<D>(k, p.k + (long long)(s + j) * p.kv_st + g * p.kv_sh, lane);
-            row_load<D>(v, p.v + (long long)(s + j) * p.kv_st + g * p.kv_sh, lane);
-            const float x = prefill_logit(p, row_dot<D>(q, k), i, j, s, g, slope);
-            const float mn = fmaxf(m, x), a = m == mn ? 1.f : expf(m - mn), w = x == -INFINITY ? 0.f : expf(x - mn);
-            l = l * a + w;
-            m = mn;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) o[c] = o[c] * a + w * v[c];
-        }
-        const size_t row = (size_t)(s + i) * p.Hq + h;
-        row_store<D>(p.o + row * D, o, l == 0.f ? 0.f : 1.f / l, lane);
-        if (lane == 0 && p.lse != nullptr) p.lse[row] = m + logf(l);
-    }
-}
-
+// grid: (documents, heads, blocks of rows); 8 rows per block step
 // dq and delta, one warp per query row
 template <int D>
 __global__ void __launch_bounds__(256) prefill_dq_rows_kernel(const __grid_constant__ PrefillParams p) {

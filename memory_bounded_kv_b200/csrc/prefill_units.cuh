@@ -1,0 +1,178 @@
+// Work units and score arithmetic shared by the prompt-attention kernels.
+#pragma once
+
+#include "tc5.cuh"
+
+namespace kvb {
+
+struct PrefillParams {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    const float* lb;          // log beta or null
+    const int* cu;            // [N + 1]
+    const int* prefix;        // [N] or null
+    long long q_st, q_sh, kv_st, kv_sh, lb_st, lb_sh;   // element strides of a token and of a head
+    int T, N, Hq, Hkv, G;
+    float scale, softcap;     // softcap 0: no cap
+    uint16_t* o;              // [T, Hq, d] bf16
+    float* lse;               // [T, Hq] or null
+    unsigned long long wait_ns;
+    // gradients
+    const uint16_t* d_o;      // [T, Hq, d]
+    const float* d_lse;       // [T, Hq] or null
+    float* delta;             // [T, Hq]: sum_j p_ij (dO_i . v_j) - dlse_i
+    uint16_t* dq;             // [T, Hq, d]
+    uint16_t* dk;             // [T, Hkv, d]
+    uint16_t* dv;             // [T, Hkv, d]
+    float* dlb;               // [T, Hkv] or null
+};
+
+// Whether cu is in order and inside [0, T]; the same for the whole warp. Records KVB_DERR_RANGE if not.
+__device__ __forceinline__ bool prefill_docs_ok(const int* cu, int N, int T) {
+    bool bad = false;
+    for (int n = threadIdx.x & 31; n < N; n += 32) bad |= cu[n] < 0 || cu[n + 1] < cu[n] || cu[n + 1] > T;
+    bad = __any_sync(kFull, bad);
+    if (bad && (threadIdx.x & 31) == 0) raise_error(KVB_DERR_RANGE);
+    return !bad;
+}
+
+// A unit: block `blk` of 2^sh tokens of a document (rows s .. s + len) and a kv head.
+struct PrefillUnit {
+    int s, len, blk, g, pre;
+};
+
+// The units in an order of falling work, found from cu alone (the host does not know the lengths):
+// level b holds block b of every document that has one, for every kv head, and later blocks see more
+// keys. A whole warp walks it; the blocks of document `lane` stay in a register.
+struct PrefillWalk {
+    const int* cu;
+    const int* prefix;
+    int N, Hkv, sh, lane, t0, levels;
+    long long units;
+
+    __device__ __forceinline__ int blocks(int n) const { return n < N ? (cu[n + 1] - cu[n] + (1 << sh) - 1) >> sh : 0; }
+    // blocks of level >= b, all documents
+    __device__ __forceinline__ int count(int b) const {
+        int c = max(t0 - b, 0);
+        for (int n = lane + 32; n < N; n += 32) c += max(blocks(n) - b, 0);
+        return __reduce_add_sync(kFull, c);
+    }
+    __device__ __forceinline__ PrefillWalk(const PrefillParams& p, int sh_)
+        : cu(p.cu), prefix(p.prefix), N(p.N), Hkv(p.Hkv), sh(sh_), lane(threadIdx.x & 31) {
+        levels = t0 = blocks(lane);
+        for (int n = lane + 32; n < N; n += 32) levels = max(levels, blocks(n));
+        levels = __reduce_max_sync(kFull, levels);
+        units = (long long)count(0) * Hkv;
+    }
+    // unit u of [0, units)
+    __device__ __forceinline__ PrefillUnit unit(long long u) const {
+        int lo = 0, hi = levels;   // count(lo) * Hkv > u >= count(hi) * Hkv
+        int above = 0;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1, c = count(mid);
+            if ((long long)c * Hkv > u) {
+                lo = mid;
+            } else {
+                hi = mid;
+                above = c;
+            }
+        }
+        const long long at = u - (long long)above * Hkv;
+        int rank = (int)(at / Hkv), doc = 0;
+        for (int n0 = 0; n0 < N; n0 += 32) {
+            const bool has = (n0 == 0 ? t0 : blocks(n0 + lane)) > lo;
+            const unsigned m = __ballot_sync(kFull, has);
+            const int c = __popc(m);
+            if (rank < c) {
+                const unsigned pick = __ballot_sync(kFull, has && __popc(m & ((1u << lane) - 1u)) == rank);
+                doc = n0 + __ffs(pick) - 1;
+                break;
+            }
+            rank -= c;
+        }
+        PrefillUnit x;
+        x.s = cu[doc];
+        x.len = cu[doc + 1] - x.s;
+        x.blk = lo;
+        x.g = (int)(at % Hkv);
+        x.pre = prefix == nullptr ? 0 : min(max(prefix[doc], 0), x.len);
+        return x;
+    }
+    // the r-th unit of CTA `c` of `grid`: rounds run forth and back, so that the CTA with a round's
+    // heaviest unit gets the next round's lightest
+    __device__ __forceinline__ static long long nth(long long r, int c, int grid) {
+        return r * grid + ((r & 1) ? grid - 1 - c : c);
+    }
+};
+
+// ---- packed pairs of floats -------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void upk2(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 1 / x to about 2^-23 (PTX rcp.approx.ftz)
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh(y) = 1 - 2 / (1 + e^2y): off by about 2^-23 absolute
+__device__ __forceinline__ float tanh_exp(float y) { return 1.f - 2.f * rcp_approx(1.f + ex2_approx(2.f * kLog2e * y)); }
+
+// log beta within +-2^60 (NaN stays): -inf times a distance would meet 0 * inf, and its bf16 parts NaN
+__device__ __forceinline__ float clamp_log_beta(float x) {
+    constexpr float B = 1152921504606846976.f;
+    return x < -B ? -B : (x > B ? B : x);
+}
+
+// Shared-memory descriptor of a K-major operand without swizzle, 16 elements (two 16-byte chunks) of K:
+// 8 rows x 16 bytes are 128 contiguous bytes, the second chunk 128 bytes on, 8-row groups 256 bytes.
+__device__ __forceinline__ uint64_t umma_desc_plain16(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (8ull << 16) | (16ull << 32) | (1ull << 46);
+}
+// byte offset of chunk c (0, 1) of a row in that layout
+__host__ __device__ constexpr int plain16_off(int row, int c) { return (row >> 3) * 256 + c * 128 + (row & 7) * 16; }
+
+// Three bf16 parts of an fp32 value (24 bits, so hi + mid + lo = x), each in the low half of a word
+__device__ __forceinline__ void split3_bf16(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = pack_bf16(x, 0.f);
+    const float r = x - bf16_lo(hi);
+    mid = pack_bf16(r, 0.f);
+    lo = pack_bf16(r - bf16_lo(mid), 0.f);
+}
+
+// The bias columns of a key: with the query's (i', i', i', 1, 1, 1, 0, 0), i' = i - base, the product is
+// i' b + (base - j) b = (i - j) b, b in the units of the raw scores.
+__device__ __forceinline__ uint4 bias_columns(float b, int base_minus_j) {
+    uint32_t bh, bm, bl, ch, cm, cl;
+    split3_bf16(b, bh, bm, bl);
+    split3_bf16((float)base_minus_j * b, ch, cm, cl);
+    return make_uint4(bh | (bm << 16), bl | (ch << 16), cm | (cl << 16), 0u);
+}
+// ... and a query's: i' <= 255 is exact in bf16
+__device__ __forceinline__ uint4 bias_query(int i) {
+    const uint32_t x = pack_bf16((float)i, (float)i), one = 0x3f803f80u;
+    return make_uint4(x, (x & 0xffffu) | (one & 0xffff0000u), one, 0u);
+}
+
+}  // namespace kvb
