@@ -432,12 +432,14 @@ kvb_status kvb_paged_compact_blocks(const kvb_paged_cache* cache, const int32_t*
  * (their weight for j is 0, and 0 times it is NaN), as in the formula's
  * products.
  *
- * Requirements: d in {64, 128}; Hq / Hkv in {1, 2, 4, 8}; T <= 2^30, N <=
+ * Requirements: d in {64, 128}; Hq / Hkv in {1, 2, 4, 8}; T <=
+ * KVB_PREFILL_MAX_TOKENS (distances are exact in fp32), N <=
  * KVB_PREFILL_MAX_DOCS; q, k, v, o and the bf16 gradients 16-byte aligned;
  * the strides of q, k, v multiples of 8, at least d; scale 0 (for 1/sqrt(d))
  * or in [2^-20, 2^20]; softcap 0 or in [2^-20, 2^20].
  * ---------------------------------------------------------------------- */
 #define KVB_PREFILL_MAX_DOCS 65536
+#define KVB_PREFILL_MAX_TOKENS (1 << 24)
 #define KVB_PREFILL_MIN_SCALE (1.0f / (1 << 20))
 
 typedef struct kvb_prefill_args {

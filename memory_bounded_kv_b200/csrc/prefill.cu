@@ -6,7 +6,7 @@
 
 #include "host.cuh"
 #include "paged_fill.cuh"
-#include "prefill_attn.cuh"
+#include "prefill_bwd.cuh"
 #include "prefill_fwd.cuh"
 
 kvb_status kvb_prefill_take_error(unsigned* bits) { return take_error_word(bits); }
@@ -18,7 +18,7 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 // The host checks of kvb_prefill_attn and its gradients, and the kernels' parameters.
 kvb_status prefill_params(const kvb_prefill_args* a, kvb::PrefillParams* out) {
     if (a == nullptr) return KVB_EINVAL;
-    if (a->T < 0 || a->T > (1 << 30) || a->N < 0 || a->N > KVB_PREFILL_MAX_DOCS || a->Hq < 1 || a->Hkv < 1) return KVB_EINVAL;
+    if (a->T < 0 || a->T > KVB_PREFILL_MAX_TOKENS || a->N < 0 || a->N > KVB_PREFILL_MAX_DOCS || a->Hq < 1 || a->Hkv < 1) return KVB_EINVAL;
     if ((a->d != 64 && a->d != 128) || a->Hq % a->Hkv != 0 || a->Hq > 65535) return KVB_EINVAL;
     const int G = a->Hq / a->Hkv;
     if (G != 1 && G != 2 && G != 4 && G != 8) return KVB_EINVAL;
@@ -62,6 +62,13 @@ bool make_rows_map(CUtensorMap* map, const void* x, int d, int H, int T, long lo
 // The most units of 2^sh tokens that N documents of T tokens in all can have.
 long long most_units(const kvb::PrefillParams& p, int sh) { return ((long long)(p.T >> sh) + p.N) * p.Hkv; }
 
+// log2 of the tokens whose 256 query rows are a unit of the kernels by query rows
+int unit_shift(const kvb::PrefillParams& p) {
+    int sh = 8;
+    for (int g = p.G; g > 1; g >>= 1) --sh;
+    return sh;
+}
+
 template <int D, bool BETA, bool CAP>
 kvb_status launch_fwd(const kvb::PrefillParams& p, cudaStream_t st) {
     using SH = kvb::FwdShape<D>;
@@ -74,9 +81,7 @@ kvb_status launch_fwd(const kvb::PrefillParams& p, cudaStream_t st) {
         return KVB_EINVAL;
     const int slots = resident_ctas(kern, SH::NT, SH::SMEM);
     if (slots <= 0) return KVB_ECUDA;
-    int sh = 8;
-    for (int g = p.G; g > 1; g >>= 1) --sh;
-    const int grid = (int)std::min<long long>(slots, most_units(p, sh));
+    const int grid = (int)std::min<long long>(slots, most_units(p, unit_shift(p)));
     return launch_pdl(kern, dim3(grid), dim3(SH::NT), SH::SMEM, st, p, mq, mk, mv);
 }
 
@@ -87,11 +92,40 @@ kvb_status fwd_dispatch(const kvb::PrefillParams& p, cudaStream_t st) {
     return cap ? launch_fwd<D, false, true>(p, st) : launch_fwd<D, false, false>(p, st);
 }
 
+template <int D, bool BETA, bool CAP>
+kvb_status launch_bwd(const kvb::PrefillParams& p, cudaStream_t st) {
+    using SQ = kvb::DqShape<D>;
+    using SK = kvb::DkvShape<D>;
+    auto kq = kvb::prefill_dq_kernel<D, BETA, CAP>;
+    auto kk = kvb::prefill_dkv_kernel<D, BETA, CAP>;
+    if (set_smem(kq, SQ::SMEM) != KVB_OK || set_smem(kk, SK::SMEM) != KVB_OK) return KVB_ECUDA;
+    CUtensorMap mq, mo, mk, mv;
+    const long long ost = (long long)p.Hq * D;
+    if (!make_rows_map(&mq, p.q, D, p.Hq, p.T, p.q_sh, p.q_st, p.G, SQ::R / p.G) ||
+        !make_rows_map(&mo, p.d_o, D, p.Hq, p.T, D, ost, p.G, SQ::R / p.G) ||
+        !make_rows_map(&mk, p.k, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SQ::KT) ||
+        !make_rows_map(&mv, p.v, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SQ::KT))
+        return KVB_EINVAL;
+    int slots = resident_ctas(kq, SQ::NT, SQ::SMEM);
+    if (slots <= 0) return KVB_ECUDA;
+    int grid = (int)std::min<long long>(slots, most_units(p, unit_shift(p)));
+    if (launch_pdl(kq, dim3(grid), dim3(SQ::NT), SQ::SMEM, st, p, mq, mo, mk, mv) != KVB_OK) return KVB_ECUDA;
+    if (!make_rows_map(&mq, p.q, D, p.Hq, p.T, p.q_sh, p.q_st, p.G, SK::QT / p.G) ||
+        !make_rows_map(&mo, p.d_o, D, p.Hq, p.T, D, ost, p.G, SK::QT / p.G) ||
+        !make_rows_map(&mk, p.k, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SK::KT) ||
+        !make_rows_map(&mv, p.v, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SK::KT))
+        return KVB_EINVAL;
+    slots = resident_ctas(kk, SK::NT, SK::SMEM);
+    if (slots <= 0) return KVB_ECUDA;
+    grid = (int)std::min<long long>(slots, most_units(p, 7));
+    return launch_pdl(kk, dim3(grid), dim3(SK::NT), SK::SMEM, st, p, mq, mo, mk, mv);
+}
+
 template <int D>
-kvb_status launch_rows(const kvb::PrefillParams& p, cudaStream_t st) {
-    const dim3 grid(p.N, p.Hq, std::min(64, (p.T + 7) / 8)), kv_grid(p.N, p.Hkv, grid.z);
-    if (launch_pdl(kvb::prefill_dq_rows_kernel<D>, grid, dim3(256), 0, st, p) != KVB_OK) return KVB_ECUDA;
-    return launch_pdl(kvb::prefill_dkv_rows_kernel<D>, kv_grid, dim3(256), 0, st, p);
+kvb_status bwd_dispatch(const kvb::PrefillParams& p, cudaStream_t st) {
+    const bool beta = p.lb != nullptr, cap = p.softcap > 0.f;
+    if (beta) return cap ? launch_bwd<D, true, true>(p, st) : launch_bwd<D, true, false>(p, st);
+    return cap ? launch_bwd<D, false, true>(p, st) : launch_bwd<D, false, false>(p, st);
 }
 
 }  // namespace
@@ -123,7 +157,7 @@ kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* a, const kvb_prefill_gra
     p.d_o = g->d_o; p.d_lse = g->d_lse; p.dq = g->dq; p.dk = g->dk; p.dv = g->dv; p.dlb = g->d_log_beta;
     p.delta = static_cast<float*>(g->workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return a->d == 128 ? launch_rows<128>(p, st) : launch_rows<64>(p, st);
+    return a->d == 128 ? bwd_dispatch<128>(p, st) : bwd_dispatch<64>(p, st);
 }
 
 size_t kvb_paged_plan_workspace_bytes(int32_t B, int32_t Hkv) {

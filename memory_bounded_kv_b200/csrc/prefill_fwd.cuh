@@ -347,10 +347,10 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                             first = false;
                             if (tile == 0) umma_commit(&o_full[t]);
                         }
+                        if (t == 1) umma_commit(&v_empty[st]);
                         if (more && tile - 1 < nt) scores(t, nst, tile * KT <= (t ? i1 : i0) + 1);
                     }
                     if (stop) break;
-                    umma_commit(&v_empty[st]);
                     if (more) umma_commit(&k_empty[nst]);
                     if (tile == 1) umma_commit(q_empty);
                 }

@@ -99,7 +99,7 @@ def c_args(**kw):
     return _lib.PrefillArgs(**a)
 
 
-BAD = [dict(d=96), dict(Hq=6), dict(Hq=32), dict(Hkv=0), dict(T=-1), dict(T=(1 << 30) + 1), dict(N=-1), dict(N=65537),
+BAD = [dict(d=96), dict(Hq=6), dict(Hq=32), dict(Hkv=0), dict(T=-1), dict(T=(1 << 24) + 1), dict(N=-1), dict(N=65537),
        dict(q=None), dict(k=F + 2), dict(v=None), dict(cu=None), dict(o=F + 4), dict(log_beta=F + 2),
        dict(q_stride_t=Hq * d + 4), dict(q_stride_h=0), dict(kv_stride_t=-Hkv * d), dict(kv_stride_h=d - 8),
        dict(lb_stride_t=-1), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=2.0 ** -21), dict(scale=float("inf")),
