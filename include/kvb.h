@@ -427,10 +427,9 @@ kvb_status kvb_paged_compact_blocks(const kvb_paged_cache* cache, const int32_t*
  * Rows of no document are neither read into a result nor written. A document
  * may be empty. cu out of order or outside [0, T] sets KVB_DERR_RANGE and
  * nothing is written.
- * An infinity or a NaN in a row of q or k reaches the rows that see it, and no
- * other document. One in v_j may also reach rows i < j of the same document
- * (their weight for j is 0, and 0 times it is NaN), as in the formula's
- * products.
+ * An infinity or a NaN in a row reaches no other document. One in v_j or d_o_i
+ * may also reach pairs (i, j) of the same document that do not see each other
+ * (their weight is 0, and 0 times it is NaN), as in the formula's products.
  *
  * Requirements: d in {64, 128}; Hq / Hkv in {1, 2, 4, 8}; T <=
  * KVB_PREFILL_MAX_TOKENS (distances are exact in fp32), N <=

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
     uint64_t* q_empty = bars + 1;
     uint64_t* kv_full = bars + 2;
     uint64_t* kv_empty = kv_full + ST;
-    uint64_t* x_full = kv_empty + ST;    // the bias columns and slopes; K's rows past the document cleared
+    uint64_t* x_full = kv_empty + ST;    // the bias columns and slopes; K's and V's rows past the document cleared
     uint64_t* s_full = x_full + ST;      // [tile] S and dP
     uint64_t* ds_full = s_full + 2;
     uint64_t* o_full = ds_full + 2;      // [tile] dQ
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
             }
             if (stop && lane == 0) fail();
         } else if (warp == 10) {
-            // ======================= bias columns, K past a document's end =======================
+            // ======================= bias columns, K and V past a document's end =======================
             const float unit_b = CAP ? kLog2e : 1.f / p.scale;
             int step = 0;
             bool stop = false;
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                         if (!warp_wait(&kv_full[st], ph, p.wait_ns)) { stop = true; break; }
                         const int rows = len - tile * KT;
                         unsigned char* kt = smem + SH::KV_OFF + st * 2 * SH::KTILE;
-                        for (int x = lane; x < (KT - rows) * 8 * (D / 64); x += 32) {
-                            const int row = rows + x / (8 * (D / 64)), c = x % (8 * (D / 64));
+                        for (int x = lane; x < (KT - rows) * 16 * (D / 64); x += 32) {
+                            const int row = rows + x / (16 * (D / 64)), c = x % (16 * (D / 64));   // chunks of K, then of V
                             *reinterpret_cast<uint4*>(kt + (c >> 3) * SH::KHALF + row * 128 + ((c & 7) << 4)) =
                                 make_uint4(0u, 0u, 0u, 0u);
                         }
@@ -270,23 +270,16 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
                 int step = 0, dc0 = 0, dc1 = 0, oc0 = 0, oc1 = 0;
                 bool stop = false;
+                const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::KV_OFF);
+                const uint32_t kr_lo = desc_mn_lo(sbase + SH::KV_OFF, SH::KHALF);
+                const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
                 auto scores = [&](int t, int st, bool past) {
-                    const uint32_t qa = sbase + SH::Q_OFF + t * SH::QTILE, ka = sbase + SH::KV_OFF + st * 2 * SH::KTILE;
-                    const uint32_t tm = tmem + t * SH::TM_T;
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t qo = (kk >> 2) * SH::QHALF + (kk & 3) * 32, ko = (kk >> 2) * SH::KHALF + (kk & 3) * 32;
-                        umma_bf16(tm + SH::TM_S, umma_desc_sw128(qa + qo), umma_desc_sw128(ka + ko), idesc_s, kk > 0 ? 1u : 0u);
-                    }
+                    const uint32_t tm = tmem + t * SH::TM_T, q = q_lo + t * (SH::QTILE >> 4), k = k_lo + st * (2 * SH::KTILE >> 4);
+                    umma_kmajor<D / 16>(tm + SH::TM_S, q, SH::QHALF, k, SH::KHALF, idesc_s);
                     if (BETA && !CAP && past)
-                        umma_bf16(tm + SH::TM_S, umma_desc_plain16(sbase + SH::QX_OFF + t * R * 32),
-                                  umma_desc_plain16(sbase + SH::KX_OFF + st * KT * 32), idesc_s, 1u);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t qo = (kk >> 2) * SH::QHALF + (kk & 3) * 32, ko = (kk >> 2) * SH::KHALF + (kk & 3) * 32;
-                        umma_bf16(tm + SH::TM_DP, umma_desc_sw128(qa + 2 * SH::QTILE + qo),
-                                  umma_desc_sw128(ka + SH::KTILE + ko), idesc_s, kk > 0 ? 1u : 0u);
-                    }
+                        umma_bf16(tm + SH::TM_S, desc(qx_lo + t * (R * 32 >> 4), kDescPlainHi),
+                                  desc(kx_lo + st * (KT * 32 >> 4), kDescPlainHi), idesc_s, 1u);
+                    umma_kmajor<D / 16>(tm + SH::TM_DP, q + (2 * SH::QTILE >> 4), SH::QHALF, k + (SH::KTILE >> 4), SH::KHALF, idesc_s);
                     umma_commit(&s_full[t]);
                 };
                 auto loaded = [&](int k) {
@@ -311,7 +304,6 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                         const int st = step % ST;
                         const bool more = tile > 0;
                         if (more && !loaded(step + 1)) { stop = true; break; }
-                        const uint32_t ka = sbase + SH::KV_OFF + st * 2 * SH::KTILE;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             int& dc = t ? dc1 : dc0;
@@ -326,11 +318,8 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                                     ++oc;
                                 }
                                 tc_fence_after();
-#pragma unroll
-                                for (int kk = 0; kk < KT / 16; ++kk)
-                                    umma_bf16_ts(tmem + t * SH::TM_T + SH::TM_DQ, tmem + t * SH::TM_T + SH::TM_S + kk * 8,
-                                                 umma_desc_sw128_mn(ka + kk * 2048, SH::KHALF, 1024), idesc_o,
-                                                 first && kk == 0 ? 0u : 1u);
+                                umma_rows<KT / 16>(tmem + t * SH::TM_T + SH::TM_DQ, tmem + t * SH::TM_T + SH::TM_S,
+                                                   kr_lo + st * (2 * SH::KTILE >> 4), idesc_o, first);
                                 first = false;
                                 if (tile == 0) umma_commit(&o_full[t]);
                             }
@@ -419,6 +408,10 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                         x[c + 3] = fmaf(fmaxf(di - (c + 3), 0.f), b.w, x[c + 3]);
                     }
                 }
+                if (j0 + KT > max(first + 1, pre)) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c] = c < lim - j0 ? x[c] : -INFINITY;
+                }
                 const uint64_t c2 = pk2(C, C), n2 = pk2(-lse2, -lse2), e2 = pk2(-est, -est);
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
@@ -427,7 +420,6 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     x[c] = ex2_approx(a);
                     x[c + 1] = ex2_approx(b);
                 }
-                const bool masked = j0 + KT > max(first + 1, pre);
                 uint64_t sum = 0ull;
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
@@ -438,14 +430,6 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
                         ds[e / 2] = mul2(pk2(x[c0 + e], x[c0 + e + 1]), add2(pk2(dp[e], dp[e + 1]), e2));
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float a, b;
-                            upk2(ds[e / 2], a, b);
-                            ds[e / 2] = pk2(c0 + e < lim - j0 ? a : 0.f, c0 + e + 1 < lim - j0 ? b : 0.f);
-                        }
-                    }
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -759,23 +743,16 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 int step = 0;
                 unsigned dc = 0;   // bit t: parity of buffer t's next dS
                 bool stop = false;
+                const uint32_t k_lo = desc_sw128_lo(sbase + SH::K_OFF), q_lo = desc_sw128_lo(sbase + SH::QO_OFF);
+                const uint32_t qr_lo = desc_mn_lo(sbase + SH::QO_OFF, SH::QHALF);
+                const uint32_t kx_lo = desc_plain_lo(sbase + SH::KX_OFF), qx_lo = desc_plain_lo(sbase + SH::QX_OFF);
                 auto scores = [&](int t, int st, bool past) {
-                    const uint32_t ka = sbase + SH::K_OFF, qa = sbase + SH::QO_OFF + st * 2 * SH::QTILE;
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t qo = (kk >> 2) * SH::QHALF + (kk & 3) * 32, ko = (kk >> 2) * SH::KHALF + (kk & 3) * 32;
-                        umma_bf16(tmem + SH::TM_S + t * 64, umma_desc_sw128(ka + ko), umma_desc_sw128(qa + qo), idesc_s,
-                                  kk > 0 ? 1u : 0u);
-                    }
+                    const uint32_t ts = tmem + SH::TM_S + t * 64, q = q_lo + st * (2 * SH::QTILE >> 4);
+                    umma_kmajor<D / 16>(ts, k_lo, SH::KHALF, q, SH::QHALF, idesc_s);
                     if (BETA && !CAP && past)
-                        umma_bf16(tmem + SH::TM_S + t * 64, umma_desc_plain16(sbase + SH::KX_OFF),
-                                  umma_desc_plain16(sbase + SH::QX_OFF + st * QT * 32), idesc_s, 1u);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t qo = (kk >> 2) * SH::QHALF + (kk & 3) * 32, ko = (kk >> 2) * SH::KHALF + (kk & 3) * 32;
-                        umma_bf16(tmem + SH::TM_DP + t * 64, umma_desc_sw128(ka + SH::KTILE + ko),
-                                  umma_desc_sw128(qa + SH::QTILE + qo), idesc_s, kk > 0 ? 1u : 0u);
-                    }
+                        umma_bf16(ts, desc(kx_lo, kDescPlainHi), desc(qx_lo + st * (QT * 32 >> 4), kDescPlainHi), idesc_s, 1u);
+                    umma_kmajor<D / 16>(tmem + SH::TM_DP + t * 64, k_lo + (SH::KTILE >> 4), SH::KHALF, q + (SH::QTILE >> 4),
+                                        SH::QHALF, idesc_s);
                     umma_commit(&s_full[t]);
                 };
                 auto loaded = [&](int k) {
@@ -799,17 +776,9 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                             dc ^= 1u << t;
                             if (q == 2 && uc >= 1 && !mbar_wait(o_empty, (unsigned)(uc - 1) & 1u, p.wait_ns)) { stop = true; break; }
                             tc_fence_after();
-                            const uint32_t qa = sbase + SH::QO_OFF + st * 2 * SH::QTILE;
-#pragma unroll
-                            for (int kk = 0; kk < QT / 16; ++kk)
-                                umma_bf16_ts(tmem + SH::TM_DV, tmem + SH::TM_S + t * 64 + kk * 8,
-                                             umma_desc_sw128_mn(qa + SH::QTILE + kk * 2048, SH::QHALF, 1024), idesc_o,
-                                             q == 2 && kk == 0 ? 0u : 1u);
-#pragma unroll
-                            for (int kk = 0; kk < QT / 16; ++kk)
-                                umma_bf16_ts(tmem + SH::TM_DK, tmem + SH::TM_DP + t * 64 + kk * 8,
-                                             umma_desc_sw128_mn(qa + kk * 2048, SH::QHALF, 1024), idesc_o,
-                                             q == 2 && kk == 0 ? 0u : 1u);
+                            const uint32_t q_rows = qr_lo + st * (2 * SH::QTILE >> 4);
+                            umma_rows<QT / 16>(tmem + SH::TM_DV, tmem + SH::TM_S + t * 64, q_rows + (SH::QTILE >> 4), idesc_o, q == 2);
+                            umma_rows<QT / 16>(tmem + SH::TM_DK, tmem + SH::TM_DP + t * 64, q_rows, idesc_o, q == 2);
                             umma_commit(&q_empty[st]);
                         }
                         if (q < n) {
@@ -910,12 +879,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        uint64_t ds = mul2(pk2(x[c0 + e], x[c0 + e + 1]), add2(pk2(dp[e], dp[e + 1]), pk2(dl[e], dl[e + 1])));
-                        float a, b;
-                        if (!past) {
-                            upk2(ds, a, b);
-                            ds = pk2(c0 + e >= from ? a : 0.f, c0 + e + 1 >= from ? b : 0.f);
-                        }
+                        const uint64_t ds = mul2(pk2(x[c0 + e], x[c0 + e + 1]), add2(pk2(dp[e], dp[e + 1]), pk2(dl[e], dl[e + 1])));
                         if (BETA) {
                             const float2 k2 = reinterpret_cast<const float2*>(tok4)[(c0 + e) / 2];
                             if (past) {
@@ -925,6 +889,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                                 sumt = fma2(ds, pk2(fmaxf(di + k2.x, 0.f), fmaxf(di + k2.y, 0.f)), sumt);
                             }
                         }
+                        float a, b;
                         upk2(ds, a, b);
                         if (CAP) {
                             a *= 1.f - th[c0 + e] * th[c0 + e];

@@ -286,17 +286,15 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
             int step = 0, pc0 = 0, pc1 = 0, oc0 = 0, oc1 = 0;
             unsigned fixes = 0;   // bit st: parity of the next clearing of stage st
             bool stop = false;
+            const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::K_OFF);
+            const uint32_t v_lo = desc_mn_lo(sbase + SH::V_OFF, SH::HALF);
+            const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
             auto scores = [&](int t, int st, bool past) {
-                const uint32_t qa = sbase + SH::Q_OFF + t * SH::TILE, ka = sbase + SH::K_OFF + st * SH::TILE;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * SH::HALF + (kk & 3) * 32;
-                    umma_bf16(tmem + SH::TM_S + t * 128, umma_desc_sw128(qa + off), umma_desc_sw128(ka + off), idesc_s,
-                              kk > 0 ? 1u : 0u);
-                }
+                const uint32_t ts = tmem + SH::TM_S + t * 128;
+                umma_kmajor<D / 16>(ts, q_lo + t * (SH::TILE >> 4), SH::HALF, k_lo + st * (SH::TILE >> 4), SH::HALF, idesc_s);
                 if (BETA && !CAP && past)
-                    umma_bf16(tmem + SH::TM_S + t * 128, umma_desc_plain16(sbase + SH::QX_OFF + t * SH::XCOL),
-                              umma_desc_plain16(sbase + SH::KX_OFF + st * SH::XCOL), idesc_s, 1u);
+                    umma_bf16(ts, desc(qx_lo + t * (SH::XCOL >> 4), kDescPlainHi), desc(kx_lo + st * (SH::XCOL >> 4), kDescPlainHi),
+                              idesc_s, 1u);
                 umma_commit(&s_full[t]);
             };
             for (int uc = 0; !stop; ++uc) {
@@ -324,7 +322,6 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                         if (!mbar_wait(&v_fix[st], (fixes >> st) & 1u, p.wait_ns)) { stop = true; break; }
                         fixes ^= 1u << st;
                     }
-                    const uint32_t va = sbase + SH::V_OFF + st * SH::TILE;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         int& pc = t ? pc1 : pc0;
@@ -339,11 +336,8 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                                 ++oc;
                             }
                             tc_fence_after();
-#pragma unroll
-                            for (int kk = 0; kk < KT / 16; ++kk)
-                                umma_bf16_ts(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128 + kk * 8,
-                                             umma_desc_sw128_mn(va + kk * 2048, SH::HALF, 1024), idesc_o,
-                                             first && kk == 0 ? 0u : 1u);
+                            umma_rows<KT / 16>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128,
+                                               v_lo + st * (SH::TILE >> 4), idesc_o, first);
                             first = false;
                             if (tile == 0) umma_commit(&o_full[t]);
                         }
@@ -387,32 +381,39 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
             for (int tile = nt - 1; tile >= 0; --tile, ++step, ++sc) {
                 if (!warp_wait(&s_full[t], (unsigned)sc & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
+                const int j0 = tile * KT, st = step % ST;
+                const bool biased = BETA && (CAP || j0 + KT > first + 1), masked = j0 + KT > max(first + 1, pre);
+                if (CAP || biased || masked) {
+                    // the cap, the bias and the mask of these tiles go into S itself
+                    if (biased && !warp_wait(&lb_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                    const float4* lb = reinterpret_cast<const float4*>(smem + SH::LB_OFF + st * KT * 4);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < KT; c0 += 32) {
+                        float y[32];
+                        tmem_ld32(ts + c0, y);
+                        tmem_ld_wait();
+                        const float di = (float)(i - j0 - c0);
+                        const int seen = lim - j0 - c0;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 b = biased ? lb[(c0 + c) / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+                            const float bs[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float a = y[c + e];
+                                if (CAP) a = cap2 * tanh_exp(a * per_cap);
+                                if (BETA) a = fmaf(fmaxf(di - (c + e), 0.f), bs[e], a);
+                                y[c + e] = c + e < seen ? a : -INFINITY;
+                            }
+                        }
+                        tmem_st32(ts + c0, reinterpret_cast<const uint32_t*>(y));
+                    }
+                    tmem_st_wait();
+                }
                 float x[128];
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) tmem_ld32(ts + c, x + c);
                 tmem_ld_wait();
-                const int j0 = tile * KT, st = step % ST;
-                if (CAP) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) x[c] = cap2 * tanh_exp(x[c] * per_cap);
-                }
-                if (BETA && (CAP || j0 + KT > first + 1)) {
-                    if (!warp_wait(&lb_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
-                    const float4* lb = reinterpret_cast<const float4*>(smem + SH::LB_OFF + st * KT * 4);
-                    const float di = (float)(i - j0);
-#pragma unroll
-                    for (int c = 0; c < 128; c += 4) {
-                        const float4 b = lb[c / 4];
-                        x[c] = fmaf(fmaxf(di - c, 0.f), b.x, x[c]);
-                        x[c + 1] = fmaf(fmaxf(di - (c + 1), 0.f), b.y, x[c + 1]);
-                        x[c + 2] = fmaf(fmaxf(di - (c + 2), 0.f), b.z, x[c + 2]);
-                        x[c + 3] = fmaf(fmaxf(di - (c + 3), 0.f), b.w, x[c + 3]);
-                    }
-                }
-                if (j0 + KT > max(first + 1, pre)) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) x[c] = c < lim - j0 ? x[c] : -INFINITY;
-                }
                 float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                 for (int c = 4; c < 128; c += 4)

@@ -145,10 +145,36 @@ __device__ __forceinline__ float clamp_log_beta(float x) {
     return x < -B ? -B : (x > B ? B : x);
 }
 
-// Shared-memory descriptor of a K-major operand without swizzle, 16 elements (two 16-byte chunks) of K:
-// 8 rows x 16 bytes are 128 contiguous bytes, the second chunk 128 bytes on, 8-row groups 256 bytes.
-__device__ __forceinline__ uint64_t umma_desc_plain16(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (8ull << 16) | (16ull << 32) | (1ull << 46);
+// Shared-memory descriptors, low word (address / 16, leading byte offset) and high word apart: one
+// thread issues every product, and a product's operands differ in the low word by a constant.
+//   sw128: K-major, 128-byte swizzle (rows of 128 bytes, 8-row groups of 1024)
+//   mn:    MN-major, 128-byte swizzle, groups of 64 elements `half` bytes apart, 8-row groups of 1024
+//   plain: K-major without swizzle, 16 elements of K: 8 rows x 16 bytes are 128 contiguous bytes, the
+//          second 16-byte chunk of K 128 bytes on, 8-row groups 256 bytes
+constexpr uint32_t kDescSw128Hi = 64u | (1u << 14) | (2u << 29), kDescPlainHi = 16u | (1u << 14);
+__device__ __forceinline__ uint32_t desc_sw128_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn_lo(uint32_t saddr, uint32_t half) { return (saddr >> 4) | ((half >> 4) << 16); }
+__device__ __forceinline__ uint32_t desc_plain_lo(uint32_t saddr) { return (saddr >> 4) | (8u << 16); }
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+// D (+)= A B^T over K = 16 * STEPS; a, b: low words of K-major 128-byte-swizzled operands whose 64-wide
+// halves are `ah`, `bh` bytes apart
+template <int STEPS>
+__device__ __forceinline__ void umma_kmajor(uint32_t d, uint32_t a, uint32_t ah, uint32_t b, uint32_t bh, uint32_t idesc) {
+#pragma unroll
+    for (int kk = 0; kk < STEPS; ++kk)
+        umma_bf16(d, desc(a + (((kk >> 2) * ah + (kk & 3) * 32) >> 4), kDescSw128Hi),
+                  desc(b + (((kk >> 2) * bh + (kk & 3) * 32) >> 4), kDescSw128Hi), idesc, kk > 0 ? 1u : 0u);
+}
+// D (+)= A B over K = 16 * STEPS rows of B (MN-major, 128 bytes a row and half), A in tensor memory
+template <int STEPS>
+__device__ __forceinline__ void umma_rows(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool fresh) {
+#pragma unroll
+    for (int kk = 0; kk < STEPS; ++kk)
+        umma_bf16_ts(d, a_tmem + kk * 8, desc(b + kk * 128, kDescSw128Hi), idesc, kk > 0 || !fresh ? 1u : 0u);
 }
 // byte offset of chunk c (0, 1) of a row in that layout
 __host__ __device__ constexpr int plain16_off(int row, int c) { return (row >> 3) * 256 + c * 128 + (row & 7) * 16; }
