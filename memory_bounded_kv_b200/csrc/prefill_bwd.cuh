@@ -21,22 +21,25 @@
 
 namespace kvb {
 
-// The bias columns of the key side, where one block of keys meets queries at any distance: with
-// i - last = a0 + 256 a1 + 65536 a2 (each factor exact in bf16, tokens <= 2^24) the product is
-// (i - last) b + (last - j) b, both terms of one sign.
-__device__ __forceinline__ void far_bias_query(int dist, uint4& c0, uint4& c1) {
+// The extra columns of prefill_dkv_kernel, where one block of keys meets queries at any distance: with
+// i - last = a0 + 256 a1 + 65536 a2 (each term exact in bf16, tokens <= 2^24) and the three bf16 parts
+// of b, of (last - j) b and of a per-query number y (- lse / scale for S, - delta for dP) the product is
+// (i - last) b + (last - j) b + y; both terms of the bias have one sign.
+__device__ __forceinline__ void far_query(int dist, float y, uint4& c0, uint4& c1) {
     const uint32_t a0 = pack_bf16((float)(dist & 255), (float)(dist & 255));
     const uint32_t a1 = pack_bf16((float)(dist & 0xff00), (float)(dist & 0xff00));
     const uint32_t a2 = pack_bf16((float)(dist & 0xff0000), (float)(dist & 0xff0000)), one = 0x3f803f80u;
+    uint32_t yh, ym, yl;
+    split3_bf16(y, yh, ym, yl);
     c0 = make_uint4(a0, (a0 & 0xffffu) | (a1 & 0xffff0000u), a1, a2);
-    c1 = make_uint4((a2 & 0xffffu) | (one & 0xffff0000u), one, 0u, 0u);
+    c1 = make_uint4((a2 & 0xffffu) | (one & 0xffff0000u), one, yh | (ym << 16), yl);
 }
-__device__ __forceinline__ void far_bias_key(float b, int last_minus_j, uint4& c0, uint4& c1) {
+__device__ __forceinline__ void far_key(float b, int last_minus_j, uint4& c0, uint4& c1) {
     uint32_t h, m, l, ch, cm, cl;
     split3_bf16(b, h, m, l);
     split3_bf16((float)last_minus_j * b, ch, cm, cl);
     c0 = make_uint4(h | (m << 16), l | (h << 16), m | (l << 16), h | (m << 16));
-    c1 = make_uint4(l | (ch << 16), cm | (cl << 16), 0u, 0u);
+    c1 = make_uint4(l | (ch << 16), cm | (cl << 16), 0x3f803f80u, 0x3f80u);
 }
 
 template <int D>
@@ -265,73 +268,80 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
             }
             if (stop && lane == 0) fail();
         } else if (warp == 8) {
-            // ======================= products (one lane) =======================
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
-                int step = 0, dc0 = 0, dc1 = 0, oc0 = 0, oc1 = 0;
-                bool stop = false;
-                const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::KV_OFF);
-                const uint32_t kr_lo = desc_mn_lo(sbase + SH::KV_OFF, SH::KHALF);
-                const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
-                auto scores = [&](int t, int st, bool past) {
-                    const uint32_t tm = tmem + t * SH::TM_T, q = q_lo + t * (SH::QTILE >> 4), k = k_lo + st * (2 * SH::KTILE >> 4);
-                    umma_kmajor<D / 16>(tm + SH::TM_S, q, SH::QHALF, k, SH::KHALF, idesc_s);
-                    if (BETA && !CAP && past)
-                        umma_bf16(tm + SH::TM_S, desc(qx_lo + t * (R * 32 >> 4), kDescPlainHi),
-                                  desc(kx_lo + st * (KT * 32 >> 4), kDescPlainHi), idesc_s, 1u);
-                    umma_kmajor<D / 16>(tm + SH::TM_DP, q + (2 * SH::QTILE >> 4), SH::QHALF, k + (SH::KTILE >> 4), SH::KHALF, idesc_s);
-                    umma_commit(&s_full[t]);
-                };
-                auto loaded = [&](int k) {
-                    return mbar_wait(&kv_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns) &&
-                           mbar_wait(&x_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns);
-                };
-                for (int uc = 0; !stop; ++uc) {
-                    const int ub = uc & 1;
-                    if (!mbar_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { fail(); break; }
-                    const int* m = info + ub * 8;
-                    const int s = m[0], i0 = m[2], n0 = m[5], n1 = m[6];
-                    mbar_arrive(&u_empty[ub]);
-                    if (s < 0) break;
-                    const int n = max(n0, n1), i1 = i0 + (1 << (sh - 1));
-                    if (!mbar_wait(q_full, (unsigned)uc & 1u, p.wait_ns) || !loaded(step)) { fail(); break; }
-                    tc_fence_after();
+            // ======================= products =======================
+            // the warp stays together (its values are uniform); one lane issues
+            constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
+            int step = 0;
+            unsigned dc = 0;           // bit t: parity of tile t's next dS
+            int oc0 = 0, oc1 = 0;
+            bool stop = false;
+            const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::KV_OFF);
+            const uint32_t kr_lo = desc_mn_lo(sbase + SH::KV_OFF, SH::KHALF);
+            const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
+            auto scores = [&](int t, int st, bool past) {
+                const uint32_t tm = tmem + t * SH::TM_T, q = q_lo + t * (SH::QTILE >> 4), k = k_lo + st * (2 * SH::KTILE >> 4);
+                umma_kmajor<D / 16>(tm + SH::TM_S, q, SH::QHALF, k, SH::KHALF, idesc_s);
+                if (BETA && !CAP && past)
+                    umma_bf16(tm + SH::TM_S, desc(qx_lo + t * (R * 32 >> 4), kDescPlainHi),
+                              desc(kx_lo + st * (KT * 32 >> 4), kDescPlainHi), idesc_s, 1u);
+                umma_kmajor<D / 16>(tm + SH::TM_DP, q + (2 * SH::QTILE >> 4), SH::QHALF, k + (SH::KTILE >> 4), SH::KHALF, idesc_s);
+                umma_commit(&s_full[t]);
+            };
+            auto loaded = [&](int k) {
+                return warp_wait(&kv_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns) &&
+                       warp_wait(&x_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns);
+            };
+            for (int uc = 0; !stop; ++uc) {
+                const int ub = uc & 1;
+                if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
+                const int* m = info + ub * 8;
+                const int s = __shfl_sync(kFull, m[0], 0), i0 = __shfl_sync(kFull, m[2], 0);
+                const int n0 = __shfl_sync(kFull, m[5], 0), n1 = __shfl_sync(kFull, m[6], 0);
+                if (lane == 0) mbar_arrive(&u_empty[ub]);
+                if (s < 0) break;
+                const int n = max(n0, n1), i1 = i0 + (1 << (sh - 1));
+                if (!warp_wait(q_full, (unsigned)uc & 1u, p.wait_ns) || !loaded(step)) { stop = true; break; }
+                tc_fence_after();
+                if (elect_one()) {
                     if (n - 1 < n0) scores(0, step % ST, n * KT <= i0 + 1);
                     if (n - 1 < n1) scores(1, step % ST, n * KT <= i1 + 1);
                     if (n == 1) umma_commit(q_empty);
-                    bool first0 = true, first1 = true;
-                    for (int tile = n - 1; tile >= 0; --tile, ++step) {
-                        const int st = step % ST;
-                        const bool more = tile > 0;
-                        if (more && !loaded(step + 1)) { stop = true; break; }
+                }
+                __syncwarp();
+                for (int tile = n - 1; tile >= 0; --tile, ++step) {
+                    const int st = step % ST;
+                    const bool more = tile > 0;
+                    if (more && !loaded(step + 1)) { stop = true; break; }
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            int& dc = t ? dc1 : dc0;
-                            int& oc = t ? oc1 : oc0;
-                            bool& first = t ? first1 : first0;
-                            const int nt = t ? n1 : n0;
-                            if (tile < nt) {
-                                if (!mbar_wait(&ds_full[t], (unsigned)dc & 1u, p.wait_ns)) { stop = true; break; }
-                                ++dc;
-                                if (first) {
-                                    if (oc > 0 && !mbar_wait(&o_empty[t], (unsigned)(oc - 1) & 1u, p.wait_ns)) { stop = true; break; }
-                                    ++oc;
-                                }
-                                tc_fence_after();
+                    for (int t = 0; t < 2; ++t) {
+                        const int nt = t ? n1 : n0;
+                        const bool have = tile < nt, first = tile == nt - 1;
+                        if (have) {
+                            if (!warp_wait(&ds_full[t], (dc >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                            dc ^= 1u << t;
+                            if (first) {
+                                int& oc = t ? oc1 : oc0;
+                                if (oc > 0 && !warp_wait(&o_empty[t], (unsigned)(oc - 1) & 1u, p.wait_ns)) { stop = true; break; }
+                                ++oc;
+                            }
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (have) {
                                 umma_rows<KT / 16>(tmem + t * SH::TM_T + SH::TM_DQ, tmem + t * SH::TM_T + SH::TM_S,
                                                    kr_lo + st * (2 * SH::KTILE >> 4), idesc_o, first);
-                                first = false;
                                 if (tile == 0) umma_commit(&o_full[t]);
                             }
                             if (t == 1) umma_commit(&kv_empty[st]);
                             if (more && tile - 1 < nt) scores(t, (step + 1) % ST, tile * KT <= (t ? i1 : i0) + 1);
+                            if (t == 1 && tile == 1) umma_commit(q_empty);
                         }
-                        if (stop) break;
-                        if (tile == 1) umma_commit(q_empty);
+                        __syncwarp();
                     }
-                    if (stop) fail();
+                    if (stop) break;
                 }
             }
+            if (stop && lane == 0) fail();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REG_SOFT));
@@ -481,8 +491,9 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8 && lane == 0) {
-        umma_commit(fin);
+    if (warp == 8) {
+        if (elect_one()) umma_commit(fin);   // by the lane that issued the products
+        __syncwarp();
         mbar_wait(fin, 0u, p.wait_ns);
     }
     if (tid == 0 && *s_abort) {
@@ -508,9 +519,10 @@ struct DkvShape {
     static constexpr int K_OFF = 0;                      // K, V
     static constexpr int QO_OFF = K_OFF + 2 * KTILE;     // [ST] Q, dO
     static constexpr int KX_OFF = QO_OFF + ST * 2 * QTILE;
-    static constexpr int QX_OFF = KX_OFF + KT * 32;      // [ST]
-    static constexpr int ROW_OFF = QX_OFF + ST * QT * 32;   // [ST][64] (lse in log2 units, delta)
-    static constexpr int TOK_OFF = ROW_OFF + ST * QT * 8;   // [64] token of a row within the step, as float
+    static constexpr int ONE_OFF = KX_OFF + KT * 32;     // key columns without a bias
+    static constexpr int QX_OFF = ONE_OFF + KT * 32;     // [ST] extra columns of Q, of dO
+    static constexpr int ROW_OFF = QX_OFF + ST * 2 * QT * 32;   // [ST][64] lse in log2 units
+    static constexpr int TOK_OFF = ROW_OFF + ST * QT * 4;   // [64] token of a row within the step, as float
     static constexpr int DB_OFF = TOK_OFF + QT * 4;      // [128] d log beta of the second warpgroup's steps
     static constexpr int INFO_OFF = DB_OFF + KT * 4;
     static constexpr int BAR_OFF = INFO_OFF + 2 * 8 * 4;
@@ -576,6 +588,11 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
         fence_mbar_init();
     }
     if (tid < QT) reinterpret_cast<float*>(smem + SH::TOK_OFF)[tid] = (float)(tid >> lg);
+    if (tid < KT) {
+        *reinterpret_cast<uint4*>(smem + SH::ONE_OFF + plain16_off(tid, 0)) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(smem + SH::ONE_OFF + plain16_off(tid, 1)) = make_uint4(0u, 0u, 0x3f803f80u, 0x3f80u);
+    }
+    fence_proxy_async_smem();
     if (warp == 9 && lane == 0) {
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmO);
@@ -688,7 +705,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     for (int e = 0; e < 4; ++e) {
                         const int c = lane + 32 * e;
                         uint4 c0, c1;
-                        far_bias_key(b[e], last - j0 - c, c0, c1);
+                        far_key(b[e], last - j0 - c, c0, c1);
                         *reinterpret_cast<uint4*>(smem + SH::KX_OFF + plain16_off(c, 0)) = c0;
                         *reinterpret_cast<uint4*>(smem + SH::KX_OFF + plain16_off(c, 1)) = c1;
                     }
@@ -696,28 +713,34 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 for (int blk = b0; blk < b1; ++blk, ++step) {
                     const int st = step % ST;
                     const unsigned ph = (unsigned)(step / ST) & 1u;
-                    float2 v[2];
+                    float lse[2], delta[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int c = lane + 32 * e, i = blk * bt + (c >> lg);
-                        v[e] = make_float2(INFINITY, 0.f);   // no such row: P = 0
+                        lse[e] = 1.2676506e30f;   // no such row (2^100): P = 0
+                        delta[e] = 0.f;
                         if (i < len) {
                             const size_t row = (size_t)(s + i) * p.Hq + (g << lg) + (c & (p.G - 1));
-                            v[e] = make_float2(p.lse[row] * kLog2e, p.delta[row]);
+                            lse[e] = p.lse[row];
+                            delta[e] = p.delta[row];
                         }
                     }
                     if (step >= ST && !warp_wait(&q_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int c = lane + 32 * e;
-                        reinterpret_cast<float2*>(smem + SH::ROW_OFF)[st * QT + c] = v[e];
-                        if (BETA && !CAP) {
-                            uint4 c0, c1;
-                            far_bias_query(max(blk * bt + (c >> lg) - last, 0), c0, c1);
-                            unsigned char* at = smem + SH::QX_OFF + st * QT * 32;
+                        uint4 c0, c1;
+                        unsigned char* at = smem + SH::QX_OFF + st * 2 * QT * 32;
+                        if (CAP) {
+                            reinterpret_cast<float*>(smem + SH::ROW_OFF)[st * QT + c] = lse[e] * kLog2e;
+                        } else {
+                            far_query(BETA ? max(blk * bt + (c >> lg) - last, 0) : 0, lse[e] * (-1.f / p.scale), c0, c1);
                             *reinterpret_cast<uint4*>(at + plain16_off(c, 0)) = c0;
                             *reinterpret_cast<uint4*>(at + plain16_off(c, 1)) = c1;
                         }
+                        far_query(0, -delta[e], c0, c1);
+                        *reinterpret_cast<uint4*>(at + QT * 32 + plain16_off(c, 0)) = c0;
+                        *reinterpret_cast<uint4*>(at + QT * 32 + plain16_off(c, 1)) = c1;
                     }
                     if ((blk + 1) * bt > len) {
                         if (!warp_wait(&q_full[st], ph, p.wait_ns)) { stop = true; break; }
@@ -737,62 +760,69 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             }
             if (stop && lane == 0) fail();
         } else if (warp == 8) {
-            // ======================= products (one lane) =======================
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = umma_idesc_bf16(KT, QT), idesc_o = umma_idesc_bf16_bmn(KT, D);
-                int step = 0;
-                unsigned dc = 0;   // bit t: parity of buffer t's next dS
-                bool stop = false;
-                const uint32_t k_lo = desc_sw128_lo(sbase + SH::K_OFF), q_lo = desc_sw128_lo(sbase + SH::QO_OFF);
-                const uint32_t qr_lo = desc_mn_lo(sbase + SH::QO_OFF, SH::QHALF);
-                const uint32_t kx_lo = desc_plain_lo(sbase + SH::KX_OFF), qx_lo = desc_plain_lo(sbase + SH::QX_OFF);
-                auto scores = [&](int t, int st, bool past) {
-                    const uint32_t ts = tmem + SH::TM_S + t * 64, q = q_lo + st * (2 * SH::QTILE >> 4);
-                    umma_kmajor<D / 16>(ts, k_lo, SH::KHALF, q, SH::QHALF, idesc_s);
-                    if (BETA && !CAP && past)
-                        umma_bf16(ts, desc(kx_lo, kDescPlainHi), desc(qx_lo + st * (QT * 32 >> 4), kDescPlainHi), idesc_s, 1u);
-                    umma_kmajor<D / 16>(tmem + SH::TM_DP + t * 64, k_lo + (SH::KTILE >> 4), SH::KHALF, q + (SH::QTILE >> 4),
-                                        SH::QHALF, idesc_s);
-                    umma_commit(&s_full[t]);
-                };
-                auto loaded = [&](int k) {
-                    return mbar_wait(&q_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns) &&
-                           mbar_wait(&x_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns);
-                };
-                for (int uc = 0; !stop; ++uc) {
-                    const int ub = uc & 1;
-                    if (!mbar_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { fail(); break; }
-                    const int* m = info + ub * 8;
-                    const int s = m[0], j0 = m[2], b0 = m[5], b1 = m[6];
-                    mbar_arrive(&u_empty[ub]);
-                    if (s < 0) break;
-                    const int n = b1 - b0, last = j0 + KT - 1;
-                    if (!mbar_wait(k_full, (unsigned)uc & 1u, p.wait_ns)) { fail(); break; }
-                    for (int q = 0; q < n + 2; ++q) {
-                        // step q - 2's gradients free buffer q % 2 for step q's scores
+            // ======================= products =======================
+            // the warp stays together (its values are uniform); one lane issues
+            constexpr uint32_t idesc_s = umma_idesc_bf16(KT, QT), idesc_o = umma_idesc_bf16_bmn(KT, D);
+            int step = 0;
+            unsigned dc = 0;   // bit t: parity of buffer t's next dS
+            bool stop = false;
+            const uint32_t k_lo = desc_sw128_lo(sbase + SH::K_OFF), q_lo = desc_sw128_lo(sbase + SH::QO_OFF);
+            const uint32_t qr_lo = desc_mn_lo(sbase + SH::QO_OFF, SH::QHALF);
+            const uint32_t kx_lo = desc_plain_lo(sbase + SH::KX_OFF), qx_lo = desc_plain_lo(sbase + SH::QX_OFF);
+            const uint32_t one_lo = desc_plain_lo(sbase + SH::ONE_OFF);
+            auto scores = [&](int t, int st, bool past) {
+                const uint32_t ts = tmem + SH::TM_S + t * 64, q = q_lo + st * (2 * SH::QTILE >> 4);
+                const uint32_t qx = qx_lo + st * (2 * QT * 32 >> 4);
+                umma_kmajor<D / 16>(ts, k_lo, SH::KHALF, q, SH::QHALF, idesc_s);
+                if (!CAP)   // - lse, and the bias where every query is past every key
+                    umma_bf16(ts, desc(BETA && past ? kx_lo : one_lo, kDescPlainHi), desc(qx, kDescPlainHi), idesc_s, 1u);
+                umma_kmajor<D / 16>(tmem + SH::TM_DP + t * 64, k_lo + (SH::KTILE >> 4), SH::KHALF, q + (SH::QTILE >> 4),
+                                    SH::QHALF, idesc_s);
+                umma_bf16(tmem + SH::TM_DP + t * 64, desc(one_lo, kDescPlainHi), desc(qx + (QT * 32 >> 4), kDescPlainHi),
+                          idesc_s, 1u);   // - delta
+                umma_commit(&s_full[t]);
+            };
+            auto loaded = [&](int k) {
+                return warp_wait(&q_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns) &&
+                       warp_wait(&x_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns);
+            };
+            for (int uc = 0; !stop; ++uc) {
+                const int ub = uc & 1;
+                if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
+                const int* m = info + ub * 8;
+                const int s = __shfl_sync(kFull, m[0], 0), j0 = __shfl_sync(kFull, m[2], 0);
+                const int b0 = __shfl_sync(kFull, m[5], 0), b1 = __shfl_sync(kFull, m[6], 0);
+                if (lane == 0) mbar_arrive(&u_empty[ub]);
+                if (s < 0) break;
+                const int n = b1 - b0, last = j0 + KT - 1;
+                if (!warp_wait(k_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
+                for (int q = 0; q < n + 2; ++q) {
+                    // step q - 2's gradients free buffer q % 2 for step q's scores
+                    const int k = step + q - 2, t = q & 1, st = (k + ST) % ST;
+                    if (q >= 2) {
+                        if (!warp_wait(&ds_full[t], (dc >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                        dc ^= 1u << t;
+                        if (q == 2 && uc >= 1 && !warp_wait(o_empty, (unsigned)(uc - 1) & 1u, p.wait_ns)) { stop = true; break; }
+                    }
+                    if (q < n && !loaded(step + q)) { stop = true; break; }
+                    tc_fence_after();
+                    if (elect_one()) {
                         if (q >= 2) {
-                            const int k = step + q - 2, t = q & 1, st = k % ST;
-                            if (!mbar_wait(&ds_full[t], (dc >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                            dc ^= 1u << t;
-                            if (q == 2 && uc >= 1 && !mbar_wait(o_empty, (unsigned)(uc - 1) & 1u, p.wait_ns)) { stop = true; break; }
-                            tc_fence_after();
                             const uint32_t q_rows = qr_lo + st * (2 * SH::QTILE >> 4);
                             umma_rows<QT / 16>(tmem + SH::TM_DV, tmem + SH::TM_S + t * 64, q_rows + (SH::QTILE >> 4), idesc_o, q == 2);
                             umma_rows<QT / 16>(tmem + SH::TM_DK, tmem + SH::TM_DP + t * 64, q_rows, idesc_o, q == 2);
                             umma_commit(&q_empty[st]);
                         }
-                        if (q < n) {
-                            if (!loaded(step + q)) { stop = true; break; }
-                            tc_fence_after();
-                            scores(q & 1, (step + q) % ST, (b0 + q) * bt >= last);
-                            if (q == n - 1) umma_commit(k_empty);
-                        }
+                        if (q < n) scores(t, (step + q) % ST, (b0 + q) * bt >= last);
+                        if (q == n - 1) umma_commit(k_empty);
+                        if (q == n + 1) umma_commit(o_full);
                     }
-                    if (stop) { fail(); break; }
-                    umma_commit(o_full);
-                    step += n;
+                    __syncwarp();
                 }
+                if (stop) break;
+                step += n;
             }
+            if (stop && lane == 0) fail();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REG_SOFT));
@@ -832,10 +862,16 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 const bool past = tb >= last;
                 const float di = (float)(tb - j);
                 if (CAP) {
+                    const float4* l4 = reinterpret_cast<const float4*>(smem + SH::ROW_OFF + st * QT * 4);
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        th[c] = tanh_exp(x[c] * per_cap);
-                        x[c] = cap2 * th[c];
+                    for (int c = 0; c < 64; c += 4) {
+                        const float4 l = l4[c / 4];
+                        const float ls[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            th[c + e] = tanh_exp(x[c + e] * per_cap);
+                            x[c + e] = fmaf(cap2, th[c + e], -ls[e]);
+                        }
                     }
                 }
                 if (BETA && (CAP || !past)) {
@@ -848,45 +884,40 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         x[c + 3] = fmaf(fmaxf(di + k4.w, 0.f), slope_b, x[c + 3]);
                     }
                 }
-                const float4* rows = reinterpret_cast<const float4*>(smem + SH::ROW_OFF + st * QT * 8);   // two rows each
-                const int from = (past || j < pre) ? 0 : min(max(j - tb, 0) << lg, QT);   // the first row that sees key j
+                if (!past) {
+                    const int from = j < pre ? 0 : min(max(j - tb, 0) << lg, QT);   // the first row that sees key j
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c] = c >= from ? x[c] : -INFINITY;
+                }
                 const uint64_t c2 = pk2(C, C);
-                uint64_t sum = 0ull, sumt = 0ull;
+                // d log beta: where all is past, sum dS (di + tok(c)) with tok(c) = c >> lg, from the eight
+                // sums over c = e mod 8 and from sum (c / 8) dS; else the distances one by one
+                uint64_t by8[4] = {0ull, 0ull, 0ull, 0ull}, up = 0ull;
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
                     float dp[32];
                     tmem_ld32(tl + SH::TM_DP + t * 64 + c0, dp);
                     uint32_t w[16];
-                    float dl[32];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float4 v = rows[(c0 + e) / 2];
                         float a, b;
-                        upk2(fma2(pk2(x[c0 + e], x[c0 + e + 1]), c2, pk2(-v.x, -v.z)), a, b);
-                        a = ex2_approx(a);
-                        b = ex2_approx(b);
-                        if (!past) {
-                            a = c0 + e >= from ? a : 0.f;
-                            b = c0 + e + 1 >= from ? b : 0.f;
-                        }
-                        x[c0 + e] = a;
-                        x[c0 + e + 1] = b;
-                        dl[e] = -v.y;
-                        dl[e + 1] = -v.w;
-                        w[e / 2] = pack_bf16(a, b);
+                        upk2(mul2(pk2(x[c0 + e], x[c0 + e + 1]), c2), a, b);
+                        x[c0 + e] = ex2_approx(a);
+                        x[c0 + e + 1] = ex2_approx(b);
+                        w[e / 2] = pack_bf16(x[c0 + e], x[c0 + e + 1]);
                     }
                     tmem_st16(tl + SH::TM_S + t * 64 + c0 / 2, w);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const uint64_t ds = mul2(pk2(x[c0 + e], x[c0 + e + 1]), add2(pk2(dp[e], dp[e + 1]), pk2(dl[e], dl[e + 1])));
+                        const uint64_t ds = mul2(pk2(x[c0 + e], x[c0 + e + 1]), pk2(dp[e], dp[e + 1]));
                         if (BETA) {
-                            const float2 k2 = reinterpret_cast<const float2*>(tok4)[(c0 + e) / 2];
                             if (past) {
-                                sum = add2(sum, ds);
-                                sumt = fma2(ds, pk2(k2.x, k2.y), sumt);
+                                by8[(e / 2) & 3] = add2(by8[(e / 2) & 3], ds);
+                                up = fma2(ds, pk2((float)((c0 + e) / 8), (float)((c0 + e) / 8)), up);
                             } else {
-                                sumt = fma2(ds, pk2(fmaxf(di + k2.x, 0.f), fmaxf(di + k2.y, 0.f)), sumt);
+                                const float2 k2 = reinterpret_cast<const float2*>(tok4)[(c0 + e) / 2];
+                                up = fma2(ds, pk2(fmaxf(di + k2.x, 0.f), fmaxf(di + k2.y, 0.f)), up);
                             }
                         }
                         float a, b;
@@ -900,10 +931,22 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     tmem_st16(tl + SH::TM_DP + t * 64 + c0 / 2, w);
                 }
                 if (BETA) {
-                    float a, b, d, e;
-                    upk2(sum, a, b);
-                    upk2(sumt, d, e);
-                    db += (d + e) + (a + b) * di;   // di where every row is past; the sum is 0 elsewhere
+                    float u0, u1;
+                    upk2(up, u0, u1);
+                    if (past) {
+                        float part = (u0 + u1) * (float)(8 >> lg), all = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            float a, b;
+                            upk2(by8[e / 2], a, b);
+                            all += a + b;
+                            part = fmaf(a, (float)(e >> lg), part);
+                            part = fmaf(b, (float)((e + 1) >> lg), part);
+                        }
+                        db += fmaf(all, di, part);
+                    } else {
+                        db += u0 + u1;
+                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -948,8 +991,9 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8 && lane == 0) {
-        umma_commit(fin);
+    if (warp == 8) {
+        if (elect_one()) umma_commit(fin);   // by the lane that issued the products
+        __syncwarp();
         mbar_wait(fin, 0u, p.wait_ns);
     }
     if (tid == 0 && *s_abort) {

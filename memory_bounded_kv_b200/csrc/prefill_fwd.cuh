@@ -280,77 +280,84 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
         }
         if (stop && lane == 0) fail();
     } else if (warp == 8) {
-        // ======================= products (one lane) =======================
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
-            int step = 0, pc0 = 0, pc1 = 0, oc0 = 0, oc1 = 0;
-            unsigned fixes = 0;   // bit st: parity of the next clearing of stage st
-            bool stop = false;
-            const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::K_OFF);
-            const uint32_t v_lo = desc_mn_lo(sbase + SH::V_OFF, SH::HALF);
-            const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
-            auto scores = [&](int t, int st, bool past) {
-                const uint32_t ts = tmem + SH::TM_S + t * 128;
-                umma_kmajor<D / 16>(ts, q_lo + t * (SH::TILE >> 4), SH::HALF, k_lo + st * (SH::TILE >> 4), SH::HALF, idesc_s);
-                if (BETA && !CAP && past)
-                    umma_bf16(ts, desc(qx_lo + t * (SH::XCOL >> 4), kDescPlainHi), desc(kx_lo + st * (SH::XCOL >> 4), kDescPlainHi),
-                              idesc_s, 1u);
-                umma_commit(&s_full[t]);
-            };
-            for (int uc = 0; !stop; ++uc) {
-                const int ub = uc & 1;
-                if (!mbar_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { fail(); break; }
-                const int* m = info + ub * 8;
-                const int s = m[0], len = m[1], i0 = m[2], n0 = m[5], n1 = m[6];
-                mbar_arrive(&u_empty[ub]);
-                if (s < 0) break;
-                const int n = max(n0, n1), i1 = i0 + (1 << (sh - 1));
-                if (!mbar_wait(q_full, (unsigned)uc & 1u, p.wait_ns)) { fail(); break; }
-                if (!mbar_wait(&k_full[step % ST], (unsigned)(step / ST) & 1u, p.wait_ns)) { fail(); break; }
-                tc_fence_after();
+        // ======================= products =======================
+        // the warp stays together (its values are uniform); one lane issues
+        constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
+        int step = 0;
+        unsigned fixes = 0;           // bit st: parity of the next clearing of stage st
+        unsigned pc = 0;              // bit t: parity of tile t's next P
+        int oc0 = 0, oc1 = 0;
+        bool stop = false;
+        const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::K_OFF);
+        const uint32_t v_lo = desc_mn_lo(sbase + SH::V_OFF, SH::HALF);
+        const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
+        auto scores = [&](int t, int st, bool past) {
+            const uint32_t ts = tmem + SH::TM_S + t * 128;
+            umma_kmajor<D / 16>(ts, q_lo + t * (SH::TILE >> 4), SH::HALF, k_lo + st * (SH::TILE >> 4), SH::HALF, idesc_s);
+            if (BETA && !CAP && past)
+                umma_bf16(ts, desc(qx_lo + t * (SH::XCOL >> 4), kDescPlainHi), desc(kx_lo + st * (SH::XCOL >> 4), kDescPlainHi),
+                          idesc_s, 1u);
+            umma_commit(&s_full[t]);
+        };
+        for (int uc = 0; !stop; ++uc) {
+            const int ub = uc & 1;
+            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
+            const int* m = info + ub * 8;
+            const int s = __shfl_sync(kFull, m[0], 0), len = __shfl_sync(kFull, m[1], 0), i0 = __shfl_sync(kFull, m[2], 0);
+            const int n0 = __shfl_sync(kFull, m[5], 0), n1 = __shfl_sync(kFull, m[6], 0);
+            if (lane == 0) mbar_arrive(&u_empty[ub]);
+            if (s < 0) break;
+            const int n = max(n0, n1), i1 = i0 + (1 << (sh - 1));
+            if (!warp_wait(q_full, (unsigned)uc & 1u, p.wait_ns) ||
+                !warp_wait(&k_full[step % ST], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+            tc_fence_after();
+            if (elect_one()) {
                 if (n - 1 < n0) scores(0, step % ST, n * KT <= i0 + 1);
                 if (n - 1 < n1) scores(1, step % ST, n * KT <= i1 + 1);
                 umma_commit(&k_empty[step % ST]);
                 if (n == 1) umma_commit(q_empty);
-                bool first0 = true, first1 = true;
-                for (int tile = n - 1; tile >= 0; --tile, ++step) {
-                    const int st = step % ST, nst = (step + 1) % ST;
-                    const bool more = tile > 0;
-                    if (more && !mbar_wait(&k_full[nst], (unsigned)((step + 1) / ST) & 1u, p.wait_ns)) { stop = true; break; }
-                    if (!mbar_wait(&v_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
-                    if ((tile + 1) * KT > len) {
-                        if (!mbar_wait(&v_fix[st], (fixes >> st) & 1u, p.wait_ns)) { stop = true; break; }
-                        fixes ^= 1u << st;
-                    }
+            }
+            __syncwarp();
+            for (int tile = n - 1; tile >= 0; --tile, ++step) {
+                const int st = step % ST, nst = (step + 1) % ST;
+                const bool more = tile > 0;
+                if (more && !warp_wait(&k_full[nst], (unsigned)((step + 1) / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                if (!warp_wait(&v_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                if ((tile + 1) * KT > len) {
+                    if (!warp_wait(&v_fix[st], (fixes >> st) & 1u, p.wait_ns)) { stop = true; break; }
+                    fixes ^= 1u << st;
+                }
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        int& pc = t ? pc1 : pc0;
-                        int& oc = t ? oc1 : oc0;
-                        bool& first = t ? first1 : first0;
-                        const int nt = t ? n1 : n0;
-                        if (tile < nt) {
-                            if (!mbar_wait(&p_full[t], (unsigned)pc & 1u, p.wait_ns)) { stop = true; break; }
-                            ++pc;
-                            if (first) {
-                                if (oc > 0 && !mbar_wait(&o_empty[t], (unsigned)(oc - 1) & 1u, p.wait_ns)) { stop = true; break; }
-                                ++oc;
-                            }
-                            tc_fence_after();
+                for (int t = 0; t < 2; ++t) {
+                    const int nt = t ? n1 : n0;
+                    const bool have = tile < nt, first = tile == nt - 1;
+                    if (have) {
+                        if (!warp_wait(&p_full[t], (pc >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                        pc ^= 1u << t;
+                        if (first) {
+                            int& oc = t ? oc1 : oc0;
+                            if (oc > 0 && !warp_wait(&o_empty[t], (unsigned)(oc - 1) & 1u, p.wait_ns)) { stop = true; break; }
+                            ++oc;
+                        }
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (have) {
                             umma_rows<KT / 16>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128,
                                                v_lo + st * (SH::TILE >> 4), idesc_o, first);
-                            first = false;
                             if (tile == 0) umma_commit(&o_full[t]);
                         }
                         if (t == 1) umma_commit(&v_empty[st]);
                         if (more && tile - 1 < nt) scores(t, nst, tile * KT <= (t ? i1 : i0) + 1);
+                        if (t == 1 && more) umma_commit(&k_empty[nst]);
+                        if (t == 1 && tile == 1) umma_commit(q_empty);
                     }
-                    if (stop) break;
-                    if (more) umma_commit(&k_empty[nst]);
-                    if (tile == 1) umma_commit(q_empty);
+                    __syncwarp();
                 }
-                if (stop) fail();
+                if (stop) break;
             }
         }
+        if (stop && lane == 0) fail();
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REG_SOFT));
@@ -494,8 +501,9 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8 && lane == 0) {
-        umma_commit(fin);
+    if (warp == 8) {
+        if (elect_one()) umma_commit(fin);   // by the lane that issued the products
+        __syncwarp();
         mbar_wait(fin, 0u, p.wait_ns);
     }
     if (tid == 0 && *s_abort) {

@@ -141,6 +141,15 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// True in one lane of a converged warp. A branch on it tells the compiler that one lane issues what is
+// inside: tensor-core instructions take uniform registers, and under any other condition every one of
+// them sits in a loop over the lanes that might be active.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x != 0;
+}
+
 // A bounded wait whose outcome is the same for the whole warp (the warp then runs warp-collective
 // tensor-memory instructions or leaves together).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned long long ns) {
