@@ -467,22 +467,17 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
             if (!warp_wait(&o_full[t], (unsigned)oc & 1u, p.wait_ns)) { stop = true; break; }
             ++oc;
             tc_fence_after();
-            float o[D];
-#pragma unroll
-            for (int c = 0; c < D; c += 32) tmem_ld32(tb + SH::TM_DQ + c, o + c);
-            tmem_ld_wait();
+            uint4* dst = reinterpret_cast<uint4*>(p.dq + row * D);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                float o[32];
+                tmem_ld32(tb + SH::TM_DQ + c0, o);
+                tmem_ld_wait();
+                if (i < len) store_bf16x32(dst + c0 / 8, o, p.scale);
+            }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[t]);
-            if (i < len) {
-                uint4* dst = reinterpret_cast<uint4*>(p.dq + row * D);
-#pragma unroll
-                for (int c = 0; c < D; c += 8)
-                    dst[c / 8] = make_uint4(pack_bf16(o[c] * p.scale, o[c + 1] * p.scale),
-                                            pack_bf16(o[c + 2] * p.scale, o[c + 3] * p.scale),
-                                            pack_bf16(o[c + 4] * p.scale, o[c + 5] * p.scale),
-                                            pack_bf16(o[c + 6] * p.scale, o[c + 7] * p.scale));
-            }
+            if (lane == 0) mbar_arrive(&o_empty[t]);   // the next unit's product may overwrite dQ
         }
         if (stop && lane == 0) fail();
     }
@@ -957,10 +952,14 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             step += n;
             if (!warp_wait(o_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
             tc_fence_after();
-            float o[D];
-#pragma unroll
-            for (int c = 0; c < D; c += 32) tmem_ld32(tl + (t ? SH::TM_DK : SH::TM_DV) + c, o + c);
-            tmem_ld_wait();
+            uint4* dst = reinterpret_cast<uint4*>((t ? p.dk : p.dv) + ((size_t)(s + j) * p.Hkv + g) * D);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                float o[32];
+                tmem_ld32(tl + (t ? SH::TM_DK : SH::TM_DV) + c0, o);
+                tmem_ld_wait();
+                if (j < len) store_bf16x32(dst + c0 / 8, o, t ? p.scale : 1.f);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_empty);
@@ -974,14 +973,6 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     if (!warp_wait(db_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
                     if (j < len) p.dlb[(size_t)(s + j) * p.Hkv + g] = db + s_db[r];
                 }
-            }
-            if (j < len) {
-                const float f = t ? p.scale : 1.f;
-                uint4* dst = reinterpret_cast<uint4*>((t ? p.dk : p.dv) + ((size_t)(s + j) * p.Hkv + g) * D);
-#pragma unroll
-                for (int c = 0; c < D; c += 8)
-                    dst[c / 8] = make_uint4(pack_bf16(o[c] * f, o[c + 1] * f), pack_bf16(o[c + 2] * f, o[c + 3] * f),
-                                            pack_bf16(o[c + 4] * f, o[c + 5] * f), pack_bf16(o[c + 6] * f, o[c + 7] * f));
             }
         }
         if (stop && lane == 0) fail();

@@ -46,7 +46,7 @@ struct FwdShape {
     static constexpr int LB_OFF = KX_OFF + ST * XCOL;    // [ST][128] f32: the bias slope of each key
     static constexpr int INFO_OFF = LB_OFF + ST * KT * 4;   // [2][8] unit records
     static constexpr int BAR_OFF = INFO_OFF + 2 * 8 * 4;
-    static constexpr int NBAR = 2 + 6 * ST + 8 + 4;
+    static constexpr int NBAR = 2 + 6 * ST + 10 + 4;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr size_t SMEM = 1024 + MISC_OFF + 32;
     static constexpr int TM_S = 0, TM_O = 256, TM_COLS = 512;
@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
     uint64_t* v_fix = v_empty + ST;     // the tile's rows past the document are cleared
     uint64_t* lb_full = v_fix + ST;
     uint64_t* s_full = lb_full + ST;    // [tile]
-    uint64_t* p_full = s_full + 2;
+    uint64_t* p_half = s_full + 2;      // the weights of a tile's first 64 keys, all of them
+    uint64_t* p_full = p_half + 2;
     uint64_t* o_full = p_full + 2;
     uint64_t* o_empty = o_full + 2;
     uint64_t* u_full = o_empty + 2;     // [2] unit records
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
+            mbar_init(&p_half[t], 4);
             mbar_init(&p_full[t], 4);
             mbar_init(&o_full[t], 1);
             mbar_init(&o_empty[t], 4);
@@ -332,19 +334,25 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                     const int nt = t ? n1 : n0;
                     const bool have = tile < nt, first = tile == nt - 1;
                     if (have) {
-                        if (!warp_wait(&p_full[t], (pc >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                        pc ^= 1u << t;
                         if (first) {
                             int& oc = t ? oc1 : oc0;
                             if (oc > 0 && !warp_wait(&o_empty[t], (unsigned)(oc - 1) & 1u, p.wait_ns)) { stop = true; break; }
                             ++oc;
                         }
+                        if (!warp_wait(&p_half[t], (pc >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                        tc_fence_after();
+                        if (elect_one())
+                            umma_rows<KT / 32>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128,
+                                               v_lo + st * (SH::TILE >> 4), idesc_o, first);
+                        __syncwarp();
+                        if (!warp_wait(&p_full[t], (pc >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                        pc ^= 1u << t;
                     }
                     tc_fence_after();
                     if (elect_one()) {
                         if (have) {
-                            umma_rows<KT / 16>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128,
-                                               v_lo + st * (SH::TILE >> 4), idesc_o, first);
+                            umma_rows<KT / 32>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128 + 32,
+                                               v_lo + st * (SH::TILE >> 4) + 64 * 128 / 16, idesc_o, false);
                             if (tile == 0) umma_commit(&o_full[t]);
                         }
                         if (t == 1) umma_commit(&v_empty[st]);
@@ -423,10 +431,10 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                 tmem_ld_wait();
                 float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int c = 4; c < 128; c += 4)
+                for (int c = 4; c < 124; c += 8)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[c + e]);
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + 2 * e], x[c + 2 * e + 1]);
+                const float mt = max3(max3(mx[0], x[124], x[125]), max3(mx[1], x[126], x[127]), fmaxf(mx[2], mx[3]));
                 // the reference moves when the row's maximum passes it by more than 2^8: P <= 256, and O is
                 // rescaled (read, scaled, written back in tensor memory) only then. P V(tile + 1) is done:
                 // its product was issued before this S.
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                 const bool resc = grow && m_ref != -INFINITY;
                 if (__any_sync(kFull, resc)) {
                     const float alpha = resc ? ex2_approx((m_ref - mt) * C) : 1.f;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
                         tmem_ld32(to + c, o);
@@ -457,12 +465,23 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                     for (int e = 0; e < 32; e += 2) {
                         float a, b;
                         upk2(fma2(pk2(x[c + e], x[c + e + 1]), c2, n2), a, b);
-                        a = ex2_approx(a);
-                        b = ex2_approx(b);
+                        if (e % 8 == 6) {   // a quarter of the exponentials on the FMA pipe
+                            exp2_poly2(a, b);
+                        } else {
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                        }
                         sum = add2(sum, pk2(a, b));
                         w[e / 2] = pack_bf16(a, b);   // weights enter P V as bf16: 2^-9 each, as the output's own rounding
                     }
                     tmem_st16(ts + c / 2, w);
+                    if (c == 32) {
+                        // the first half's product starts while the second half is computed
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_half[t]);
+                    }
                 }
                 float s0, s1;
                 upk2(sum, s0, s1);
@@ -476,23 +495,20 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
             if (!warp_wait(&o_full[t], (unsigned)oc & 1u, p.wait_ns)) { stop = true; break; }
             ++oc;
             tc_fence_after();
-            float o[D];
-#pragma unroll
-            for (int c = 0; c < D; c += 32) tmem_ld32(to + c, o + c);
-            tmem_ld_wait();
+            const size_t row = (size_t)(s + i) * p.Hq + (g << lg) + (r & (p.G - 1));
+            const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+            uint4* dst = reinterpret_cast<uint4*>(p.o + row * D);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                float o[32];
+                tmem_ld32(to + c0, o);
+                tmem_ld_wait();
+                if (i < len) store_bf16x32(dst + c0 / 8, o, inv);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_empty[t]);   // the next unit's product may overwrite O
-            if (i < len) {
-                const size_t row = (size_t)(s + i) * p.Hq + (g << lg) + (r & (p.G - 1));
-                const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
-                uint4* dst = reinterpret_cast<uint4*>(p.o + row * D);
-#pragma unroll
-                for (int c = 0; c < D; c += 8)
-                    dst[c / 8] = make_uint4(pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
-                                            pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv));
-                if (p.lse != nullptr) p.lse[row] = (m_ref * C + log2f(l_sum)) * kLn2;
-            }
+            if (i < len && p.lse != nullptr) p.lse[row] = (m_ref * C + log2f(l_sum)) * kLn2;
         }
         if (stop && lane == 0) fail();
     }
