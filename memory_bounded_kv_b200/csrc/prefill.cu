@@ -100,18 +100,15 @@ kvb_status launch_bwd(const kvb::PrefillParams& p, cudaStream_t st) {
     auto kk = kvb::prefill_dkv_kernel<D, BETA, CAP>;
     if (set_smem(kq, SQ::SMEM) != KVB_OK || set_smem(kk, SK::SMEM) != KVB_OK) return KVB_ECUDA;
     CUtensorMap mq, mo, mk, mv;
-    const long long ost = (long long)p.Hq * D;
-    if (!make_rows_map(&mq, p.q, D, p.Hq, p.T, p.q_sh, p.q_st, p.G, SQ::R / p.G) ||
-        !make_rows_map(&mo, p.d_o, D, p.Hq, p.T, D, ost, p.G, SQ::R / p.G) ||
-        !make_rows_map(&mk, p.k, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SQ::KT) ||
+    if (!make_rows_map(&mk, p.k, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SQ::KT) ||
         !make_rows_map(&mv, p.v, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SQ::KT))
         return KVB_EINVAL;
     int slots = resident_ctas(kq, SQ::NT, SQ::SMEM);
     if (slots <= 0) return KVB_ECUDA;
-    int grid = (int)std::min<long long>(slots, most_units(p, unit_shift(p)));
-    if (launch_pdl(kq, dim3(grid), dim3(SQ::NT), SQ::SMEM, st, p, mq, mo, mk, mv) != KVB_OK) return KVB_ECUDA;
+    int grid = (int)std::min<long long>(slots, most_units(p, unit_shift(p) - 1));
+    if (launch_pdl(kq, dim3(grid), dim3(SQ::NT), SQ::SMEM, st, p, mk, mv) != KVB_OK) return KVB_ECUDA;
     if (!make_rows_map(&mq, p.q, D, p.Hq, p.T, p.q_sh, p.q_st, p.G, SK::QT / p.G) ||
-        !make_rows_map(&mo, p.d_o, D, p.Hq, p.T, D, ost, p.G, SK::QT / p.G) ||
+        !make_rows_map(&mo, p.d_o, D, p.Hq, p.T, D, (long long)p.Hq * D, p.G, SK::QT / p.G) ||
         !make_rows_map(&mk, p.k, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SK::KT) ||
         !make_rows_map(&mv, p.v, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SK::KT))
         return KVB_EINVAL;

@@ -12,9 +12,17 @@
 // so e_i + their sum - dlse_i is delta to fp32, for one addition per score. dq, held in bf16 itself,
 // keeps the estimate.
 //
-// In both, key or query steps of 64 give every S and dP a 128 x 64 accumulator, and two of each pair
-// are in flight: while a warpgroup turns one pair into P and dS, the products of the other run. The
-// bias rides the S product as in prefill_fwd_kernel.
+// What bounds both is shared memory and the hand-over between products and softmax. A product of two
+// shared-memory operands reads 16 (128 + N) x 2 bytes per K step of 16: at N = 64 that is 48 clocks of
+// the 128 bytes a clock for 32 clocks of mathematics, at N = 128 it is 64 for 64 (measured: 48.8 and
+// 64.4 clocks a step; with the first operand in tensor memory 32.7 and 63.4).
+//   By query rows, the block's Q and dO live in tensor memory (written there once per unit), so that
+// steps of 64 keys cost no more than their mathematics; two S and dP pairs are in flight, one per
+// warpgroup: while it turns its pair into dS, the products of the other run.
+//   By keys there is no room for that (dK, dV, S and dP fill the tensor memory), so steps take 128 query
+// rows. S and dP alternate: P done -> dV += P^T dO and the next S, while the warpgroups turn dP into dS;
+// dS done -> dK += dS^T Q and the next dP, while they turn the next S into P.
+// The bias rides the S product as in prefill_fwd_kernel; by keys, - lse and - delta ride S and dP too.
 #pragma once
 
 #include "prefill_units.cuh"
@@ -45,29 +53,27 @@ __device__ __forceinline__ void far_key(float b, int last_minus_j, uint4& c0, ui
 template <int D>
 struct DqShape {
     static constexpr int R = 128, KT = 64;
-    static constexpr int ST = D == 128 ? 2 : 4;
+    static constexpr int ST = D == 128 ? 5 : 8;          // K/V ring stages
     static constexpr int NT = 12 * 32;
-    static constexpr int REG_SOFT = 208, REG_REST = 88;
-    static constexpr int QHALF = R * 128, QTILE = QHALF * (D / 64);
+    static constexpr int REG_SOFT = 208, REG_REST = 88;  // 2 x 208 + 88 = 3 x 168, the launch's registers
     static constexpr int KHALF = KT * 128, KTILE = KHALF * (D / 64);
-    static constexpr int Q_OFF = 0;                      // Q of both tiles, then dO of both
-    static constexpr int KV_OFF = Q_OFF + 4 * QTILE;     // [ST] K, V
+    static constexpr int KV_OFF = 0;                     // [ST] K, V
     static constexpr int QX_OFF = KV_OFF + ST * 2 * KTILE;
-    static constexpr int KX_OFF = QX_OFF + 2 * R * 32;
+    static constexpr int KX_OFF = QX_OFF + R * 32;
     static constexpr int LB_OFF = KX_OFF + ST * KT * 32;
-    static constexpr int INFO_OFF = LB_OFF + ST * KT * 4;
+    static constexpr int EST_OFF = LB_OFF + ST * KT * 4; // [128] estimates, [128] row sums of the second warpgroup
+    static constexpr int INFO_OFF = EST_OFF + 2 * R * 4;
     static constexpr int BAR_OFF = INFO_OFF + 2 * 8 * 4;
-    static constexpr int NBAR = 2 + 3 * ST + 8 + 4;
+    static constexpr int NBAR = 4 + 3 * ST + 4 + 4;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr size_t SMEM = 1024 + MISC_OFF + 32;
-    static constexpr int TM_T = 256, TM_S = 0, TM_DP = 64, TM_DQ = 128, TM_COLS = 512;
+    static constexpr int TM_Q = 0, TM_DO = 64, TM_S = 128, TM_DP = 256, TM_DQ = 384, TM_COLS = 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 template <int D, bool BETA, bool CAP>
 __global__ void __launch_bounds__(DqShape<D>::NT, 1)
-    prefill_dq_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmQ,
-                      const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmK,
+    prefill_dq_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
     using SH = DqShape<D>;
     constexpr int ST = SH::ST, R = SH::R, KT = SH::KT;
@@ -76,16 +82,16 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SH::BAR_OFF);
-    uint64_t* q_full = bars;
-    uint64_t* q_empty = bars + 1;
-    uint64_t* kv_full = bars + 2;
+    uint64_t* a_full = bars;             // Q and dO are in tensor memory, the previous dQ is read
+    uint64_t* est_full = bars + 1;
+    uint64_t* sum_full = bars + 2;
+    uint64_t* o_full = bars + 3;         // dQ
+    uint64_t* kv_full = bars + 4;
     uint64_t* kv_empty = kv_full + ST;
     uint64_t* x_full = kv_empty + ST;    // the bias columns and slopes; K's and V's rows past the document cleared
-    uint64_t* s_full = x_full + ST;      // [tile] S and dP
+    uint64_t* s_full = x_full + ST;      // [buffer] S and dP
     uint64_t* ds_full = s_full + 2;
-    uint64_t* o_full = ds_full + 2;      // [tile] dQ
-    uint64_t* o_empty = o_full + 2;
-    uint64_t* u_full = o_empty + 2;
+    uint64_t* u_full = ds_full + 2;
     uint64_t* u_empty = u_full + 2;
     int* info = reinterpret_cast<int*>(smem + SH::INFO_OFF);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + SH::MISC_OFF);
@@ -94,10 +100,12 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
     uint64_t* fin = reinterpret_cast<uint64_t*>(smem + SH::MISC_OFF + 16);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int lg = 31 - __clz(p.G), sh = 8 - lg;
+    const int lg = 31 - __clz(p.G), sh = 7 - lg;        // 2^sh tokens a unit
     if (tid == 0) {
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        mbar_init(a_full, 8);
+        mbar_init(est_full, 4);
+        mbar_init(sum_full, 4);
+        mbar_init(o_full, 1);
         for (int s = 0; s < ST; ++s) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
@@ -106,27 +114,22 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&ds_full[t], 4);
-            mbar_init(&o_full[t], 1);
-            mbar_init(&o_empty[t], 4);
             mbar_init(&u_full[t], 1);
-            mbar_init(&u_empty[t], 10);
+            mbar_init(&u_empty[t], 10);   // products, bias, 8 softmax warps
         }
         mbar_init(fin, 1);
         *s_abort = 0;
-        s_steps[0] = s_steps[1] = 0;
+        s_steps[0] = 0;
         fence_mbar_init();
     }
     if (warp == 9 && lane == 0) {
-        prefetch_tensormap(&tmQ);
-        prefetch_tensormap(&tmO);
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
     if (BETA && !CAP) {
-        for (int x = tid; x < 2 * R; x += SH::NT) {
-            unsigned char* at = smem + SH::QX_OFF + (x >> 7) * R * 32;
-            *reinterpret_cast<uint4*>(at + plain16_off(x & 127, 0)) = bias_query(x >> lg);
-            *reinterpret_cast<uint4*>(at + plain16_off(x & 127, 1)) = make_uint4(0u, 0u, 0u, 0u);
+        for (int x = tid; x < R; x += SH::NT) {
+            *reinterpret_cast<uint4*>(smem + SH::QX_OFF + plain16_off(x, 0)) = bias_query(x >> lg);
+            *reinterpret_cast<uint4*>(smem + SH::QX_OFF + plain16_off(x, 1)) = make_uint4(0u, 0u, 0u, 0u);
         }
         for (int x = tid; x < ST * KT; x += SH::NT)
             *reinterpret_cast<uint4*>(smem + SH::KX_OFF + (x >> 6) * KT * 32 + plain16_off(x & 63, 1)) =
@@ -164,12 +167,10 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 const bool end = r * gridDim.x >= units;
                 if (!end && u >= units) { --uc; continue; }
                 PrefillUnit x{};
-                int n0 = 0, n1 = 0;
+                int n = 0;
                 if (!end) {
                     x = walk.unit(u);
-                    const int bt = 1 << (sh - 1), i0 = x.blk << sh, i1 = i0 + bt;
-                    n0 = (max(min(i1, x.len), x.pre) + KT - 1) / KT;
-                    n1 = i1 < x.len ? (max(min(i1 + bt, x.len), x.pre) + KT - 1) / KT : 0;
+                    n = (max(min((x.blk + 1) << sh, x.len), x.pre) + KT - 1) / KT;
                 }
                 const int ub = uc & 1;
                 if (uc >= 2 && !warp_wait(&u_empty[ub], (unsigned)((uc >> 1) - 1) & 1u, p.wait_ns)) { stop = true; break; }
@@ -181,25 +182,12 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     m[2] = x.blk << sh;
                     m[3] = x.g;
                     m[4] = x.pre;
-                    m[5] = n0;
-                    m[6] = n1;
+                    m[5] = n;
                     mbar_arrive(&u_full[ub]);
                 }
                 __syncwarp();
                 if (end) break;
-                if (uc >= 1 && !warp_wait(q_empty, (unsigned)(uc - 1) & 1u, p.wait_ns)) { stop = true; break; }
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full, (unsigned)(4 * SH::QTILE));
-                    for (int t = 0; t < 2; ++t)
-                        for (int h = 0; h < D / 64; ++h) {
-                            const int i = x.s + (x.blk << sh) + (t << (sh - 1));
-                            unsigned char* at = smem + SH::Q_OFF + t * SH::QTILE + h * SH::QHALF;
-                            tma_load_3d(at, &tmQ, 64 * h, x.g << lg, i, q_full);
-                            tma_load_3d(at + 2 * SH::QTILE, &tmO, 64 * h, x.g << lg, i, q_full);
-                        }
-                    s_steps[1] = uc + 1;
-                }
-                for (int tile = max(n0, n1) - 1; tile >= 0; --tile, ++step) {
+                for (int tile = n - 1; tile >= 0; --tile, ++step) {
                     const int st = step % ST;
                     if (step >= ST && !warp_wait(&kv_empty[st], (unsigned)((step / ST) - 1) & 1u, p.wait_ns)) { stop = true; break; }
                     if (lane == 0) {
@@ -224,7 +212,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 const int ub = uc & 1;
                 if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
                 const int* m = info + ub * 8;
-                const int s = m[0], len = m[1], i0 = m[2], g = m[3], n = max(m[5], m[6]);
+                const int s = m[0], len = m[1], i0 = m[2], g = m[3], n = m[5];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&u_empty[ub]);
                 if (s < 0) break;
@@ -272,141 +260,143 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
             // the warp stays together (its values are uniform); one lane issues
             constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
             int step = 0;
-            unsigned dc = 0;           // bit t: parity of tile t's next dS
-            int oc0 = 0, oc1 = 0;
+            unsigned dc = 0;           // bit t: parity of buffer t's next dS
             bool stop = false;
-            const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::KV_OFF);
-            const uint32_t kr_lo = desc_mn_lo(sbase + SH::KV_OFF, SH::KHALF);
+            const uint32_t k_lo = desc_sw128_lo(sbase + SH::KV_OFF), kr_lo = desc_mn_lo(sbase + SH::KV_OFF, SH::KHALF);
             const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
             auto scores = [&](int t, int st, bool past) {
-                const uint32_t tm = tmem + t * SH::TM_T, q = q_lo + t * (SH::QTILE >> 4), k = k_lo + st * (2 * SH::KTILE >> 4);
-                umma_kmajor<D / 16>(tm + SH::TM_S, q, SH::QHALF, k, SH::KHALF, idesc_s);
+                const uint32_t k = k_lo + st * (2 * SH::KTILE >> 4);
+                umma_kmajor_ts<D / 16>(tmem + SH::TM_S + t * 64, tmem + SH::TM_Q, k, SH::KHALF, idesc_s);
                 if (BETA && !CAP && past)
-                    umma_bf16(tm + SH::TM_S, desc(qx_lo + t * (R * 32 >> 4), kDescPlainHi),
-                              desc(kx_lo + st * (KT * 32 >> 4), kDescPlainHi), idesc_s, 1u);
-                umma_kmajor<D / 16>(tm + SH::TM_DP, q + (2 * SH::QTILE >> 4), SH::QHALF, k + (SH::KTILE >> 4), SH::KHALF, idesc_s);
+                    umma_bf16(tmem + SH::TM_S + t * 64, desc(qx_lo, kDescPlainHi), desc(kx_lo + st * (KT * 32 >> 4), kDescPlainHi),
+                              idesc_s, 1u);
+                umma_kmajor_ts<D / 16>(tmem + SH::TM_DP + t * 64, tmem + SH::TM_DO, k + (SH::KTILE >> 4), SH::KHALF, idesc_s);
                 umma_commit(&s_full[t]);
-            };
-            auto loaded = [&](int k) {
-                return warp_wait(&kv_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns) &&
-                       warp_wait(&x_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns);
             };
             for (int uc = 0; !stop; ++uc) {
                 const int ub = uc & 1;
                 if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
                 const int* m = info + ub * 8;
-                const int s = __shfl_sync(kFull, m[0], 0), i0 = __shfl_sync(kFull, m[2], 0);
-                const int n0 = __shfl_sync(kFull, m[5], 0), n1 = __shfl_sync(kFull, m[6], 0);
+                const int s = __shfl_sync(kFull, m[0], 0), i0 = __shfl_sync(kFull, m[2], 0), n = __shfl_sync(kFull, m[5], 0);
                 if (lane == 0) mbar_arrive(&u_empty[ub]);
                 if (s < 0) break;
-                const int n = max(n0, n1), i1 = i0 + (1 << (sh - 1));
-                if (!warp_wait(q_full, (unsigned)uc & 1u, p.wait_ns) || !loaded(step)) { stop = true; break; }
-                tc_fence_after();
-                if (elect_one()) {
-                    if (n - 1 < n0) scores(0, step % ST, n * KT <= i0 + 1);
-                    if (n - 1 < n1) scores(1, step % ST, n * KT <= i1 + 1);
-                    if (n == 1) umma_commit(q_empty);
-                }
-                __syncwarp();
-                for (int tile = n - 1; tile >= 0; --tile, ++step) {
-                    const int st = step % ST;
-                    const bool more = tile > 0;
-                    if (more && !loaded(step + 1)) { stop = true; break; }
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int nt = t ? n1 : n0;
-                        const bool have = tile < nt, first = tile == nt - 1;
-                        if (have) {
-                            if (!warp_wait(&ds_full[t], (dc >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                            dc ^= 1u << t;
-                            if (first) {
-                                int& oc = t ? oc1 : oc0;
-                                if (oc > 0 && !warp_wait(&o_empty[t], (unsigned)(oc - 1) & 1u, p.wait_ns)) { stop = true; break; }
-                                ++oc;
-                            }
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
-                            if (have) {
-                                umma_rows<KT / 16>(tmem + t * SH::TM_T + SH::TM_DQ, tmem + t * SH::TM_T + SH::TM_S,
-                                                   kr_lo + st * (2 * SH::KTILE >> 4), idesc_o, first);
-                                if (tile == 0) umma_commit(&o_full[t]);
-                            }
-                            if (t == 1) umma_commit(&kv_empty[st]);
-                            if (more && tile - 1 < nt) scores(t, (step + 1) % ST, tile * KT <= (t ? i1 : i0) + 1);
-                            if (t == 1 && tile == 1) umma_commit(q_empty);
-                        }
-                        __syncwarp();
+                if (!warp_wait(a_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
+                for (int q = 0; q < n + 2; ++q) {
+                    // step q - 2's gradient frees buffer q % 2 for step q's scores
+                    const int k = step + q, t = q & 1, st = k % ST, dst = (k + 2 * ST - 2) % ST;
+                    if (q >= 2) {
+                        if (!warp_wait(&ds_full[t], (dc >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                        dc ^= 1u << t;
                     }
-                    if (stop) break;
+                    if (q < n && (!warp_wait(&kv_full[st], (unsigned)(k / ST) & 1u, p.wait_ns) ||
+                                  !warp_wait(&x_full[st], (unsigned)(k / ST) & 1u, p.wait_ns))) { stop = true; break; }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (q >= 2) {
+                            umma_rows<KT / 16>(tmem + SH::TM_DQ, tmem + SH::TM_S + t * 64, kr_lo + dst * (2 * SH::KTILE >> 4),
+                                               idesc_o, q == 2);
+                            umma_commit(&kv_empty[dst]);
+                        }
+                        if (q < n) scores(t, st, (n - q) * KT <= i0 + 1);
+                        if (q == n + 1) umma_commit(o_full);
+                    }
+                    __syncwarp();
                 }
+                if (stop) break;
+                step += n;
             }
             if (stop && lane == 0) fail();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REG_SOFT));
-        // ======================= dS of a tile's rows, dQ and delta =======================
+        // ======================= Q and dO into tensor memory, dS, dQ and delta =======================
         const int t = warp >> 2, quarter = warp & 3;
         const int r = 32 * quarter + lane;
-        const uint32_t tb = tmem + ((uint32_t)(32 * quarter) << 16) + t * SH::TM_T;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const float C = CAP ? 1.f : p.scale * kLog2e;
         const float cap2 = CAP ? p.softcap * kLog2e : 0.f, per_cap = CAP ? p.scale / p.softcap : 0.f;
-        int sc = 0, step = 0, oc = 0;
+        float* s_est = reinterpret_cast<float*>(smem + SH::EST_OFF);
+        float* s_sum = s_est + R;
+        int sc = 0, step = 0;
         bool stop = false;
-        for (int uc = 0; !stop; ++uc) {
+        int s = -1, len = 0, i0 = 0, g = 0, pre = 0, n = 0;
+        uint32_t a[D / 2];
+        // the unit's record, and this thread's row of Q (first warpgroup) or dO (second)
+        auto next = [&](int uc) {
             const int ub = uc & 1;
-            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
+            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) return false;
             const int* m = info + ub * 8;
-            const int s = m[0], len = m[1], g = m[3], pre = m[4], n0 = m[5], n1 = m[6];
-            const int first = m[2] + (t << (sh - 1));
+            s = m[0], len = m[1], i0 = m[2], g = m[3], pre = m[4], n = m[5];
             __syncwarp();
             if (lane == 0) mbar_arrive(&u_empty[ub]);
-            if (s < 0) break;
-            const int n = max(n0, n1), nt = t ? n1 : n0;
-            const int i = first + (r >> lg);
-            const int lim = min(max(i + 1, pre), len);
-            const size_t row = (size_t)(s + i) * p.Hq + (g << lg) + (r & (p.G - 1));
-            step += n - nt;
-            if (nt == 0) continue;
-            // the estimate of delta from the output, and lse in log2 units (a row past the document: P = 0)
-            float est = 0.f, dlse = 0.f, lse2 = INFINITY;
-            if (i < len) {
-                const uint4* a = reinterpret_cast<const uint4*>(p.d_o + row * D);
-                const uint4* b = reinterpret_cast<const uint4*>(p.o + row * D);
-                float e0 = 0.f, e1 = 0.f;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    float fa[8], fb[8];
-                    unpack8(a[c], fa);
-                    unpack8(b[c], fb);
+            const int i = i0 + (r >> lg), h = (g << lg) + (r & (p.G - 1));
+            const bool row = s >= 0 && i < len;
+            const uint16_t* src = t ? p.d_o + ((size_t)(s + i) * p.Hq + h) * D : p.q + (long long)(s + i) * p.q_st + h * p.q_sh;
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        e0 = fmaf(fa[e], fb[e], e0);
-                        e1 = fmaf(fa[e + 1], fb[e + 1], e1);
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = row ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
+                a[4 * c] = v.x;
+                a[4 * c + 1] = v.y;
+                a[4 * c + 2] = v.z;
+                a[4 * c + 3] = v.w;
+            }
+            return true;
+        };
+        if (!next(0)) stop = true;
+        for (int uc = 0; !stop && s >= 0; ++uc) {
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 32) tmem_st32(tl + (t ? SH::TM_DO : SH::TM_Q) + c, a + c);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(a_full);
+            const int first = i0, i = i0 + (r >> lg);
+            const int lim = min(max(i + 1, pre), len);
+            const bool valid = i < len;
+            const size_t row = (size_t)(s + i) * p.Hq + (g << lg) + (r & (p.G - 1));
+            // the estimate of delta from the output; lse in log2 units (a row past the document: P = 0)
+            float est = 0.f, dlse = 0.f;
+            const float lse2 = valid ? p.lse[row] * kLog2e : INFINITY;
+            if (valid && p.d_lse != nullptr) dlse = p.d_lse[row];
+            if (t == 1) {
+                if (valid) {
+                    const uint4* o = reinterpret_cast<const uint4*>(p.o + row * D);
+                    float e0 = 0.f, e1 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 v = o[c];
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            e0 = fmaf(bf16_lo(a[4 * c + e]), bf16_lo(w[e]), e0);
+                            e1 = fmaf(bf16_hi(a[4 * c + e]), bf16_hi(w[e]), e1);
+                        }
                     }
+                    est = e0 + e1 - dlse;
                 }
-                if (p.d_lse != nullptr) dlse = p.d_lse[row];
-                est = e0 + e1 - dlse;
-                lse2 = p.lse[row] * kLog2e;
+                s_est[r] = est;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(est_full);
+            } else {
+                if (!warp_wait(est_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
+                est = s_est[r];
             }
             float rsum = 0.f;
-            for (int tile = nt - 1; tile >= 0; --tile, ++step, ++sc) {
+            for (int q = t; q < n; q += 2, ++sc) {
+                const int k = step + q, st = k % ST, j0 = (n - 1 - q) * KT;
                 if (!warp_wait(&s_full[t], (unsigned)sc & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
                 float x[64], th[CAP ? 64 : 1];
-                tmem_ld32(tb + SH::TM_S, x);
-                tmem_ld32(tb + SH::TM_S + 32, x + 32);
+                tmem_ld32(tl + SH::TM_S + t * 64, x);
+                tmem_ld32(tl + SH::TM_S + t * 64 + 32, x + 32);
                 tmem_ld_wait();
-                const int j0 = tile * KT, st = step % ST;
                 if (CAP) {
+                    cap_tanh<64>(x, th, per_cap);
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        th[c] = tanh_exp(x[c] * per_cap);
-                        x[c] = cap2 * th[c];
-                    }
+                    for (int c = 0; c < 64; ++c) x[c] = cap2 * th[c];
                 }
                 if (BETA && (CAP || j0 + KT > first + 1)) {
-                    if (!warp_wait(&x_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                    if (!warp_wait(&x_full[st], (unsigned)(k / ST) & 1u, p.wait_ns)) { stop = true; break; }
                     const float4* lb = reinterpret_cast<const float4*>(smem + SH::LB_OFF + st * KT * 4);
                     const float di = (float)(i - j0);
 #pragma unroll
@@ -425,34 +415,31 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 const uint64_t c2 = pk2(C, C), n2 = pk2(-lse2, -lse2), e2 = pk2(-est, -est);
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
-                    float a, b;
-                    upk2(fma2(pk2(x[c], x[c + 1]), c2, n2), a, b);
-                    x[c] = ex2_approx(a);
-                    x[c + 1] = ex2_approx(b);
+                    float u, v;
+                    upk2(fma2(pk2(x[c], x[c + 1]), c2, n2), u, v);
+                    x[c] = ex2_approx(u);
+                    x[c + 1] = ex2_approx(v);
                 }
                 uint64_t sum = 0ull;
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
                     float dp[32];
-                    tmem_ld32(tb + SH::TM_DP + c0, dp);
+                    tmem_ld32(tl + SH::TM_DP + t * 64 + c0, dp);
                     tmem_ld_wait();
-                    uint64_t ds[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        ds[e / 2] = mul2(pk2(x[c0 + e], x[c0 + e + 1]), add2(pk2(dp[e], dp[e + 1]), e2));
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        sum = add2(sum, ds[e / 2]);
-                        float a, b;
-                        upk2(ds[e / 2], a, b);
+                        const uint64_t ds = mul2(pk2(x[c0 + e], x[c0 + e + 1]), add2(pk2(dp[e], dp[e + 1]), e2));
+                        sum = add2(sum, ds);
+                        float u, v;
+                        upk2(ds, u, v);
                         if (CAP) {
-                            a *= 1.f - th[c0 + e] * th[c0 + e];
-                            b *= 1.f - th[c0 + e + 1] * th[c0 + e + 1];
+                            u *= 1.f - th[c0 + e] * th[c0 + e];
+                            v *= 1.f - th[c0 + e + 1] * th[c0 + e + 1];
                         }
-                        w[e / 2] = pack_bf16(a, b);   // dS enters dS K as bf16: 2^-9 each, as dq's own rounding
+                        w[e / 2] = pack_bf16(u, v);   // dS enters dS K as bf16: 2^-9 each, as dq's own rounding
                     }
-                    tmem_st16(tb + SH::TM_S + c0 / 2, w);
+                    tmem_st16(tl + SH::TM_S + t * 64 + c0 / 2, w);
                 }
                 float s0, s1;
                 upk2(sum, s0, s1);
@@ -463,21 +450,28 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 if (lane == 0) mbar_arrive(&ds_full[t]);
             }
             if (stop) break;
-            if (i < len) p.delta[row] = est + (rsum - dlse);
-            if (!warp_wait(&o_full[t], (unsigned)oc & 1u, p.wait_ns)) { stop = true; break; }
-            ++oc;
+            step += n;
+            if (t == 1) {
+                // the first warpgroup has begun this unit, so it has read the last one's sums
+                if (!warp_wait(a_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
+                s_sum[r] = rsum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sum_full);
+            } else {
+                if (!warp_wait(sum_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
+                if (valid) p.delta[row] = est + (rsum + s_sum[r] - dlse);
+            }
+            // the next unit's rows are on their way while this one's last product runs
+            if (!next(uc + 1) || !warp_wait(o_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
             tc_fence_after();
             uint4* dst = reinterpret_cast<uint4*>(p.dq + row * D);
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
+            for (int c0 = t * (D / 2); c0 < (t + 1) * (D / 2); c0 += 32) {
                 float o[32];
-                tmem_ld32(tb + SH::TM_DQ + c0, o);
+                tmem_ld32(tl + SH::TM_DQ + c0, o);
                 tmem_ld_wait();
-                if (i < len) store_bf16x32(dst + c0 / 8, o, p.scale);
+                if (valid) store_bf16x32(dst + c0 / 8, o, p.scale);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[t]);   // the next unit's product may overwrite dQ
         }
         if (stop && lane == 0) fail();
     }
@@ -494,7 +488,6 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
     if (tid == 0 && *s_abort) {
         for (int k = max(0, s_steps[0] - ST); k < s_steps[0]; ++k)
             mbar_wait(&kv_full[k % ST], (unsigned)(k / ST) & 1u, 100000000ull);
-        if (s_steps[1] > 0) mbar_wait(q_full, (unsigned)(s_steps[1] - 1) & 1u, 100000000ull);
     }
     __syncthreads();
     if (warp == 8) {
@@ -505,26 +498,25 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
 
 template <int D>
 struct DkvShape {
-    static constexpr int KT = 128, QT = 64;              // keys of a unit; query rows of a step (QT / G tokens)
-    static constexpr int ST = 4;
+    static constexpr int KT = 128, QT = 128;             // keys of a unit; query rows of a step (QT / G tokens)
+    static constexpr int ST = D == 128 ? 2 : 4;
     static constexpr int NT = 12 * 32;
     static constexpr int REG_SOFT = 208, REG_REST = 88;
-    static constexpr int KHALF = KT * 128, KTILE = KHALF * (D / 64);
-    static constexpr int QHALF = QT * 128, QTILE = QHALF * (D / 64);
+    static constexpr int HALF = 128 * 128, TILE = HALF * (D / 64);
     static constexpr int K_OFF = 0;                      // K, V
-    static constexpr int QO_OFF = K_OFF + 2 * KTILE;     // [ST] Q, dO
-    static constexpr int KX_OFF = QO_OFF + ST * 2 * QTILE;
+    static constexpr int QO_OFF = K_OFF + 2 * TILE;      // [ST] Q, dO
+    static constexpr int KX_OFF = QO_OFF + ST * 2 * TILE;
     static constexpr int ONE_OFF = KX_OFF + KT * 32;     // key columns without a bias
     static constexpr int QX_OFF = ONE_OFF + KT * 32;     // [ST] extra columns of Q, of dO
-    static constexpr int ROW_OFF = QX_OFF + ST * 2 * QT * 32;   // [ST][64] lse in log2 units
-    static constexpr int TOK_OFF = ROW_OFF + ST * QT * 4;   // [64] token of a row within the step, as float
-    static constexpr int DB_OFF = TOK_OFF + QT * 4;      // [128] d log beta of the second warpgroup's steps
+    static constexpr int ROW_OFF = QX_OFF + ST * 2 * QT * 32;   // [ST][128] lse in log2 units
+    static constexpr int TOK_OFF = ROW_OFF + ST * QT * 4;   // [64] token of a row within its half step, as float
+    static constexpr int DB_OFF = TOK_OFF + 64 * 4;      // [128] d log beta of the second warpgroup's columns
     static constexpr int INFO_OFF = DB_OFF + KT * 4;
     static constexpr int BAR_OFF = INFO_OFF + 2 * 8 * 4;
-    static constexpr int NBAR = 2 + 3 * ST + 7 + 4;
+    static constexpr int NBAR = 2 + 3 * ST + 6 + 4;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr size_t SMEM = 1024 + MISC_OFF + 32;
-    static constexpr int TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 384, TM_COLS = 512;   // S, dP: two of 64
+    static constexpr int TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 384, TM_COLS = 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -544,12 +536,13 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
     uint64_t* k_empty = bars + 1;
     uint64_t* q_full = bars + 2;
     uint64_t* q_empty = q_full + ST;
-    uint64_t* x_full = q_empty + ST;     // bias columns, row values; rows past the document cleared
-    uint64_t* s_full = x_full + ST;      // [buffer]
-    uint64_t* ds_full = s_full + 2;
-    uint64_t* o_full = ds_full + 2;
-    uint64_t* o_empty = o_full + 1;
-    uint64_t* db_full = o_empty + 1;     // the second warpgroup's part of d log beta
+    uint64_t* x_full = q_empty + ST;     // extra columns, row values; rows past the document cleared
+    uint64_t* s_full = x_full + ST;
+    uint64_t* dp_full = s_full + 1;
+    uint64_t* p_full = s_full + 2;
+    uint64_t* ds_full = s_full + 3;
+    uint64_t* o_full = s_full + 4;       // dV, dK
+    uint64_t* db_full = s_full + 5;      // the second warpgroup's part of d log beta
     uint64_t* u_full = db_full + 1;
     uint64_t* u_empty = u_full + 2;
     int* info = reinterpret_cast<int*>(smem + SH::INFO_OFF);
@@ -568,21 +561,22 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             mbar_init(&q_empty[s], 1);
             mbar_init(&x_full[s], 1);
         }
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(p_full, 8);
+        mbar_init(ds_full, 8);
+        mbar_init(o_full, 1);
+        mbar_init(db_full, 4);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&s_full[t], 1);
-            mbar_init(&ds_full[t], 4);
             mbar_init(&u_full[t], 1);
             mbar_init(&u_empty[t], 10);
         }
-        mbar_init(o_full, 1);
-        mbar_init(o_empty, 8);
-        mbar_init(db_full, 4);
         mbar_init(fin, 1);
         *s_abort = 0;
         s_steps[0] = s_steps[1] = 0;
         fence_mbar_init();
     }
-    if (tid < QT) reinterpret_cast<float*>(smem + SH::TOK_OFF)[tid] = (float)(tid >> lg);
+    if (tid < 64) reinterpret_cast<float*>(smem + SH::TOK_OFF)[tid] = (float)(tid >> lg);
     if (tid < KT) {
         *reinterpret_cast<uint4*>(smem + SH::ONE_OFF + plain16_off(tid, 0)) = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(smem + SH::ONE_OFF + plain16_off(tid, 1)) = make_uint4(0u, 0u, 0x3f803f80u, 0x3f80u);
@@ -651,11 +645,11 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 if (end) break;
                 if (uc >= 1 && !warp_wait(k_empty, (unsigned)(uc - 1) & 1u, p.wait_ns)) { stop = true; break; }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(k_full, (unsigned)(2 * SH::KTILE));
+                    mbar_arrive_expect_tx(k_full, (unsigned)(2 * SH::TILE));
                     for (int h = 0; h < D / 64; ++h) {
-                        unsigned char* at = smem + SH::K_OFF + h * SH::KHALF;
+                        unsigned char* at = smem + SH::K_OFF + h * SH::HALF;
                         tma_load_3d(at, &tmK, 64 * h, x.g, x.s + j0, k_full);
-                        tma_load_3d(at + SH::KTILE, &tmV, 64 * h, x.g, x.s + j0, k_full);
+                        tma_load_3d(at + SH::TILE, &tmV, 64 * h, x.g, x.s + j0, k_full);
                     }
                     s_steps[1] = uc + 1;
                 }
@@ -663,11 +657,11 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     const int st = step % ST;
                     if (step >= ST && !warp_wait(&q_empty[st], (unsigned)((step / ST) - 1) & 1u, p.wait_ns)) { stop = true; break; }
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&q_full[st], (unsigned)(2 * SH::QTILE));
+                        mbar_arrive_expect_tx(&q_full[st], (unsigned)(2 * SH::TILE));
                         for (int h = 0; h < D / 64; ++h) {
-                            unsigned char* at = smem + SH::QO_OFF + st * 2 * SH::QTILE + h * SH::QHALF;
+                            unsigned char* at = smem + SH::QO_OFF + st * 2 * SH::TILE + h * SH::HALF;
                             tma_load_3d(at, &tmQ, 64 * h, x.g << lg, x.s + b * bt, &q_full[st]);
-                            tma_load_3d(at + SH::QTILE, &tmO, 64 * h, x.g << lg, x.s + b * bt, &q_full[st]);
+                            tma_load_3d(at + SH::TILE, &tmO, 64 * h, x.g << lg, x.s + b * bt, &q_full[st]);
                         }
                         s_steps[0] = step + 1;
                     }
@@ -676,7 +670,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             }
             if (stop && lane == 0) fail();
         } else if (warp == 10) {
-            // ======================= bias columns, row values, rows past a document's end =======================
+            // ======================= extra columns, row values, rows past a document's end =======================
             int step = 0;
             bool stop = false;
             for (int uc = 0; !stop; ++uc) {
@@ -708,9 +702,9 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 for (int blk = b0; blk < b1; ++blk, ++step) {
                     const int st = step % ST;
                     const unsigned ph = (unsigned)(step / ST) & 1u;
-                    float lse[2], delta[2];
+                    float lse[4], delta[4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const int c = lane + 32 * e, i = blk * bt + (c >> lg);
                         lse[e] = 1.2676506e30f;   // no such row (2^100): P = 0
                         delta[e] = 0.f;
@@ -722,7 +716,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     }
                     if (step >= ST && !warp_wait(&q_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const int c = lane + 32 * e;
                         uint4 c0, c1;
                         unsigned char* at = smem + SH::QX_OFF + st * 2 * QT * 32;
@@ -740,10 +734,10 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     if ((blk + 1) * bt > len) {
                         if (!warp_wait(&q_full[st], ph, p.wait_ns)) { stop = true; break; }
                         const int rows = (len - blk * bt) << lg;
-                        unsigned char* qt = smem + SH::QO_OFF + st * 2 * SH::QTILE;
+                        unsigned char* qt = smem + SH::QO_OFF + st * 2 * SH::TILE;
                         for (int x = lane; x < (QT - rows) * 16 * (D / 64); x += 32) {
                             const int row = rows + x / (16 * (D / 64)), c = x % (16 * (D / 64));   // chunks of Q, then of dO
-                            *reinterpret_cast<uint4*>(qt + (c >> 3) * SH::QHALF + row * 128 + ((c & 7) << 4)) =
+                            *reinterpret_cast<uint4*>(qt + (c >> 3) * SH::HALF + row * 128 + ((c & 7) << 4)) =
                                 make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
@@ -759,23 +753,29 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             // the warp stays together (its values are uniform); one lane issues
             constexpr uint32_t idesc_s = umma_idesc_bf16(KT, QT), idesc_o = umma_idesc_bf16_bmn(KT, D);
             int step = 0;
-            unsigned dc = 0;   // bit t: parity of buffer t's next dS
             bool stop = false;
             const uint32_t k_lo = desc_sw128_lo(sbase + SH::K_OFF), q_lo = desc_sw128_lo(sbase + SH::QO_OFF);
-            const uint32_t qr_lo = desc_mn_lo(sbase + SH::QO_OFF, SH::QHALF);
+            const uint32_t qr_lo = desc_mn_lo(sbase + SH::QO_OFF, SH::HALF);
             const uint32_t kx_lo = desc_plain_lo(sbase + SH::KX_OFF), qx_lo = desc_plain_lo(sbase + SH::QX_OFF);
             const uint32_t one_lo = desc_plain_lo(sbase + SH::ONE_OFF);
-            auto scores = [&](int t, int st, bool past) {
-                const uint32_t ts = tmem + SH::TM_S + t * 64, q = q_lo + st * (2 * SH::QTILE >> 4);
-                const uint32_t qx = qx_lo + st * (2 * QT * 32 >> 4);
-                umma_kmajor<D / 16>(ts, k_lo, SH::KHALF, q, SH::QHALF, idesc_s);
+            auto scores = [&](int st, bool past) {
+                umma_kmajor<D / 16>(tmem + SH::TM_S, k_lo, SH::HALF, q_lo + st * (2 * SH::TILE >> 4), SH::HALF, idesc_s);
                 if (!CAP)   // - lse, and the bias where every query is past every key
-                    umma_bf16(ts, desc(BETA && past ? kx_lo : one_lo, kDescPlainHi), desc(qx, kDescPlainHi), idesc_s, 1u);
-                umma_kmajor<D / 16>(tmem + SH::TM_DP + t * 64, k_lo + (SH::KTILE >> 4), SH::KHALF, q + (SH::QTILE >> 4),
-                                    SH::QHALF, idesc_s);
-                umma_bf16(tmem + SH::TM_DP + t * 64, desc(one_lo, kDescPlainHi), desc(qx + (QT * 32 >> 4), kDescPlainHi),
+                    umma_bf16(tmem + SH::TM_S, desc(BETA && past ? kx_lo : one_lo, kDescPlainHi),
+                              desc(qx_lo + st * (2 * QT * 32 >> 4), kDescPlainHi), idesc_s, 1u);
+                umma_commit(s_full);
+            };
+            auto pulls = [&](int st) {
+                umma_kmajor<D / 16>(tmem + SH::TM_DP, k_lo + (SH::TILE >> 4), SH::HALF, q_lo + (st * 2 + 1) * (SH::TILE >> 4),
+                                    SH::HALF, idesc_s);
+                umma_bf16(tmem + SH::TM_DP, desc(one_lo, kDescPlainHi), desc(qx_lo + (st * 2 + 1) * (QT * 32 >> 4), kDescPlainHi),
                           idesc_s, 1u);   // - delta
-                umma_commit(&s_full[t]);
+                umma_commit(dp_full);
+            };
+            // P^T and dS^T: a warpgroup's 64 columns as 32 words at the start of its half
+            auto grad = [&](uint32_t d, uint32_t a, uint32_t b, bool fresh) {
+                umma_rows<4>(d, a, b, idesc_o, fresh);
+                umma_rows<4>(d, a + 64, b + 64 * 128 / 16, idesc_o, false);
             };
             auto loaded = [&](int k) {
                 return warp_wait(&q_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns) &&
@@ -790,46 +790,54 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 if (lane == 0) mbar_arrive(&u_empty[ub]);
                 if (s < 0) break;
                 const int n = b1 - b0, last = j0 + KT - 1;
-                if (!warp_wait(k_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
-                for (int q = 0; q < n + 2; ++q) {
-                    // step q - 2's gradients free buffer q % 2 for step q's scores
-                    const int k = step + q - 2, t = q & 1, st = (k + ST) % ST;
-                    if (q >= 2) {
-                        if (!warp_wait(&ds_full[t], (dc >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                        dc ^= 1u << t;
-                        if (q == 2 && uc >= 1 && !warp_wait(o_empty, (unsigned)(uc - 1) & 1u, p.wait_ns)) { stop = true; break; }
-                    }
-                    if (q < n && !loaded(step + q)) { stop = true; break; }
+                if (!warp_wait(k_full, (unsigned)uc & 1u, p.wait_ns) || !loaded(step)) { stop = true; break; }
+                // S and dP were read before the previous unit's last P and dS
+                tc_fence_after();
+                if (elect_one()) {
+                    scores(step % ST, b0 * bt >= last);
+                    pulls(step % ST);
+                }
+                __syncwarp();
+                for (int q = 0; q < n; ++q, ++step) {
+                    const int st = step % ST, nst = (step + 1) % ST;
+                    const bool more = q + 1 < n;
+                    const uint32_t rows = qr_lo + st * (2 * SH::TILE >> 4);
+                    if (!warp_wait(p_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
+                    tc_fence_after();
+                    if (elect_one()) grad(tmem + SH::TM_DV, tmem + SH::TM_S, rows + (SH::TILE >> 4), q == 0);
+                    __syncwarp();
+                    if (more && !loaded(step + 1)) { stop = true; break; }
+                    if (elect_one() && more) scores(nst, (b0 + q + 1) * bt >= last);
+                    __syncwarp();
+                    if (!warp_wait(ds_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                     tc_fence_after();
                     if (elect_one()) {
-                        if (q >= 2) {
-                            const uint32_t q_rows = qr_lo + st * (2 * SH::QTILE >> 4);
-                            umma_rows<QT / 16>(tmem + SH::TM_DV, tmem + SH::TM_S + t * 64, q_rows + (SH::QTILE >> 4), idesc_o, q == 2);
-                            umma_rows<QT / 16>(tmem + SH::TM_DK, tmem + SH::TM_DP + t * 64, q_rows, idesc_o, q == 2);
-                            umma_commit(&q_empty[st]);
+                        grad(tmem + SH::TM_DK, tmem + SH::TM_DP, rows, q == 0);
+                        umma_commit(&q_empty[st]);
+                        if (more) {
+                            pulls(nst);
+                        } else {
+                            umma_commit(k_empty);
+                            umma_commit(o_full);
                         }
-                        if (q < n) scores(t, (step + q) % ST, (b0 + q) * bt >= last);
-                        if (q == n - 1) umma_commit(k_empty);
-                        if (q == n + 1) umma_commit(o_full);
                     }
                     __syncwarp();
                 }
                 if (stop) break;
-                step += n;
             }
             if (stop && lane == 0) fail();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REG_SOFT));
         // ======================= P^T and dS^T of a key row; dV, dK, d log beta =======================
-        const int t = warp >> 2, quarter = warp & 3;
+        const int t = warp >> 2, quarter = warp & 3;        // columns 64 t .. of every step
         const int r = 32 * quarter + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const float C = CAP ? 1.f : p.scale * kLog2e;
         const float cap2 = CAP ? p.softcap * kLog2e : 0.f, per_cap = CAP ? p.scale / p.softcap : 0.f;
         const float4* tok4 = reinterpret_cast<const float4*>(smem + SH::TOK_OFF);
         float* s_db = reinterpret_cast<float*>(smem + SH::DB_OFF);
-        int sc = 0, step = 0;
+        int step = 0;
         bool stop = false;
         for (int uc = 0; !stop; ++uc) {
             const int ub = uc & 1;
@@ -839,34 +847,34 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&u_empty[ub]);
             if (s < 0) break;
-            const int n = b1 - b0, last = j0 + KT - 1;
+            const int last = j0 + KT - 1;
             const int j = j0 + r;
             const float slope_b = (BETA && j < len) ? clamp_log_beta(p.lb[(long long)(s + j) * p.lb_st + g * p.lb_sh]) *
                                                           (CAP ? kLog2e : 1.f / p.scale)
                                                     : 0.f;
             float db = 0.f;
-            for (int q = t; q < n; q += 2, ++sc) {
-                const int k = step + q, st = k % ST, tb = (b0 + q) * bt;   // the step's first token
-                if (!warp_wait(&s_full[t], (unsigned)sc & 1u, p.wait_ns)) { stop = true; break; }
-                if (!warp_wait(&x_full[st], (unsigned)(k / ST) & 1u, p.wait_ns)) { stop = true; break; }
+            for (int blk = b0; blk < b1; ++blk, ++step) {
+                const int st = step % ST, tb = blk * bt + ((64 * t) >> lg);   // this half's first token
+                const bool past = blk * bt >= last;
+                const float di = (float)(tb - j);
+                // ---- P
+                if (!warp_wait(s_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
                 float x[64], th[CAP ? 64 : 1];
                 tmem_ld32(tl + SH::TM_S + t * 64, x);
                 tmem_ld32(tl + SH::TM_S + t * 64 + 32, x + 32);
                 tmem_ld_wait();
-                const bool past = tb >= last;
-                const float di = (float)(tb - j);
                 if (CAP) {
-                    const float4* l4 = reinterpret_cast<const float4*>(smem + SH::ROW_OFF + st * QT * 4);
+                    if (!warp_wait(&x_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                    const float4* l4 = reinterpret_cast<const float4*>(smem + SH::ROW_OFF + (st * QT + 64 * t) * 4);
+                    cap_tanh<64>(x, th, per_cap);
 #pragma unroll
                     for (int c = 0; c < 64; c += 4) {
                         const float4 l = l4[c / 4];
-                        const float ls[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            th[c + e] = tanh_exp(x[c + e] * per_cap);
-                            x[c + e] = fmaf(cap2, th[c + e], -ls[e]);
-                        }
+                        x[c] = fmaf(cap2, th[c], -l.x);
+                        x[c + 1] = fmaf(cap2, th[c + 1], -l.y);
+                        x[c + 2] = fmaf(cap2, th[c + 2], -l.z);
+                        x[c + 3] = fmaf(cap2, th[c + 3], -l.w);
                     }
                 }
                 if (BETA && (CAP || !past)) {
@@ -880,28 +888,45 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     }
                 }
                 if (!past) {
-                    const int from = j < pre ? 0 : min(max(j - tb, 0) << lg, QT);   // the first row that sees key j
+                    const int from = j < pre ? 0 : min(max(j - tb, 0) << lg, 64);   // the first row that sees key j
 #pragma unroll
                     for (int c = 0; c < 64; ++c) x[c] = c >= from ? x[c] : -INFINITY;
                 }
                 const uint64_t c2 = pk2(C, C);
+#pragma unroll
+                for (int c0 = 0; c0 < 64; c0 += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, b;
+                        upk2(mul2(pk2(x[c0 + e], x[c0 + e + 1]), c2), a, b);
+                        if (e % 8 == 6) {   // a quarter of the exponentials on the FMA pipe
+                            exp2_poly2<5>(a, b);
+                        } else {
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                        }
+                        x[c0 + e] = a;
+                        x[c0 + e + 1] = b;
+                        w[e / 2] = pack_bf16(a, b);   // P and dS enter the gradients' products as bf16: 2^-9 each
+                    }
+                    tmem_st16(tl + SH::TM_S + t * 64 + c0 / 2, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
+                // ---- dS
+                if (!warp_wait(dp_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
+                tc_fence_after();
                 // d log beta: where all is past, sum dS (di + tok(c)) with tok(c) = c >> lg, from the eight
                 // sums over c = e mod 8 and from sum (c / 8) dS; else the distances one by one
                 uint64_t by8[4] = {0ull, 0ull, 0ull, 0ull}, up = 0ull;
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
                     float dp[32];
-                    tmem_ld32(tl + SH::TM_DP + t * 64 + c0, dp);
                     uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float a, b;
-                        upk2(mul2(pk2(x[c0 + e], x[c0 + e + 1]), c2), a, b);
-                        x[c0 + e] = ex2_approx(a);
-                        x[c0 + e + 1] = ex2_approx(b);
-                        w[e / 2] = pack_bf16(x[c0 + e], x[c0 + e + 1]);
-                    }
-                    tmem_st16(tl + SH::TM_S + t * 64 + c0 / 2, w);
+                    tmem_ld32(tl + SH::TM_DP + t * 64 + c0, dp);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -925,6 +950,10 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     }
                     tmem_st16(tl + SH::TM_DP + t * 64 + c0 / 2, w);
                 }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ds_full);
                 if (BETA) {
                     float u0, u1;
                     upk2(up, u0, u1);
@@ -943,13 +972,8 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         db += u0 + u1;
                     }
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ds_full[t]);
             }
             if (stop) break;
-            step += n;
             if (!warp_wait(o_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
             tc_fence_after();
             uint4* dst = reinterpret_cast<uint4*>((t ? p.dk : p.dv) + ((size_t)(s + j) * p.Hkv + g) * D);
@@ -960,9 +984,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 tmem_ld_wait();
                 if (j < len) store_bf16x32(dst + c0 / 8, o, t ? p.scale : 1.f);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_empty);
+            tc_fence_before();   // the next unit's products follow this thread's next P
             if (BETA) {
                 // the next unit's part is posted only after this warpgroup's steps of that unit
                 if (t == 1) {

@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                         float y[32];
                         tmem_ld32(ts + c0, y);
                         tmem_ld_wait();
+                        if (CAP) cap_tanh<32>(y, y, per_cap);
                         const float di = (float)(i - j0 - c0);
                         const int seen = lim - j0 - c0;
 #pragma unroll
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 float a = y[c + e];
-                                if (CAP) a = cap2 * tanh_exp(a * per_cap);
+                                if (CAP) a *= cap2;
                                 if (BETA) a = fmaf(fmaxf(di - (c + e), 0.f), bs[e], a);
                                 y[c + e] = c + e < seen ? a : -INFINITY;
                             }
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                         float a, b;
                         upk2(fma2(pk2(x[c + e], x[c + e + 1]), c2, n2), a, b);
                         if (e % 8 == 6) {   // a quarter of the exponentials on the FMA pipe
-                            exp2_poly2(a, b);
+                            exp2_poly2<4>(a, b);
                         } else {
                             a = ex2_approx(a);
                             b = ex2_approx(b);

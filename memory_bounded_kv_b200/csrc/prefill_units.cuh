@@ -129,20 +129,31 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t same2(float a) { return pk2(a, a); }
+
 // 2^x of a pair on the FMA pipe, for x <= 128 (below -126 as at -126): with n the nearest integer (left
-// in the low bits of x + 1.5 2^23) and f = x - n in [-1/2, 1/2], 2^f by the polynomial of degree 4 whose
-// largest relative error is smallest (2.6e-6; found by a weighted least-squares iteration), times 2^n by
-// an addition to the exponent.
+// in the low bits of x + 1.5 2^23) and f = x - n in [-1/2, 1/2], 2^f by the polynomial of degree DEG whose
+// largest relative error is smallest (4: 2.6e-6, 5: 7.5e-8; found by a weighted least-squares iteration),
+// times 2^n by an addition to the exponent.
+template <int DEG>
 __device__ __forceinline__ void exp2_poly2(float& a, float& b) {
-    constexpr float kMagic = 12582912.f;
+    static_assert(DEG == 4 || DEG == 5, "degree");
     const uint64_t x = pk2(fmaxf(a, -126.f), fmaxf(b, -126.f));
-    const uint64_t t = add2(x, pk2(kMagic, kMagic));
-    const uint64_t n = add2(t, pk2(-kMagic, -kMagic));
-    const uint64_t f = fma2(n, pk2(-1.f, -1.f), x);
-    uint64_t r = fma2(pk2(0.009570086374878883f, 0.009570086374878883f), f, pk2(0.055917851626873016f, 0.055917851626873016f));
-    r = fma2(r, f, pk2(0.240247443318367f, 0.240247443318367f));
-    r = fma2(r, f, pk2(0.6931217908859253f, 0.6931217908859253f));
-    r = fma2(r, f, pk2(0.9999992847442627f, 0.9999992847442627f));
+    const uint64_t t = add2(x, same2(12582912.f));
+    const uint64_t f = fma2(add2(t, same2(-12582912.f)), same2(-1.f), x);
+    uint64_t r;
+    if (DEG == 4) {
+        r = fma2(same2(0.009570086374878883f), f, same2(0.055917851626873016f));
+        r = fma2(r, f, same2(0.240247443318367f));
+        r = fma2(r, f, same2(0.6931217908859253f));
+        r = fma2(r, f, same2(0.9999992847442627f));
+    } else {
+        r = fma2(same2(0.0013276460813358426f), f, same2(0.009675541892647743f));
+        r = fma2(r, f, same2(0.05550713464617729f));
+        r = fma2(r, f, same2(0.24022120237350464f));
+        r = fma2(r, f, same2(0.6931469440460205f));
+        r = fma2(r, f, same2(1.0000001192092896f));
+    }
     float ta, tb;
     upk2(r, a, b);
     upk2(t, ta, tb);
@@ -175,6 +186,30 @@ __device__ __forceinline__ void store_bf16x32(uint4* dst, const float (&o)[32], 
 // tanh(y) = 1 - 2 / (1 + e^2y): off by about 2^-23 absolute
 __device__ __forceinline__ float tanh_exp(float y) { return 1.f - 2.f * rcp_approx(1.f + ex2_approx(2.f * kLog2e * y)); }
 
+// th = tanh(per_cap x): where a warp's values all lie in [-1/2, 1/2] (scores small beside the cap, the
+// common case) by y times the polynomial of degree 4 in y^2 whose largest relative error is smallest
+// (1.3e-8), which also keeps small values to fp32 accuracy; else through the exponential.
+template <int N>
+__device__ __forceinline__ void cap_tanh(const float (&x)[N], float* th, float per_cap) {
+    float most = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; c += 2) most = max3(most, fabsf(x[c]), fabsf(x[c + 1]));
+    if (__all_sync(kFull, most * per_cap <= 0.5f)) {
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            const uint64_t y = mul2(pk2(x[c], x[c + 1]), same2(per_cap)), u = mul2(y, y);
+            uint64_t r = fma2(same2(0.017135005444288254f), u, same2(-0.05298607423901558f));
+            r = fma2(r, u, same2(0.13324779272079468f));
+            r = fma2(r, u, same2(-0.3333306908607483f));
+            r = fma2(r, u, same2(1.f));
+            upk2(mul2(r, y), th[c], th[c + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c) th[c] = tanh_exp(x[c] * per_cap);
+    }
+}
+
 // log beta within +-2^60 (NaN stays): -inf times a distance would meet 0 * inf, and its bf16 parts NaN
 __device__ __forceinline__ float clamp_log_beta(float x) {
     constexpr float B = 1152921504606846976.f;
@@ -204,6 +239,13 @@ __device__ __forceinline__ void umma_kmajor(uint32_t d, uint32_t a, uint32_t ah,
     for (int kk = 0; kk < STEPS; ++kk)
         umma_bf16(d, desc(a + (((kk >> 2) * ah + (kk & 3) * 32) >> 4), kDescSw128Hi),
                   desc(b + (((kk >> 2) * bh + (kk & 3) * 32) >> 4), kDescSw128Hi), idesc, kk > 0 ? 1u : 0u);
+}
+// the same with A in tensor memory
+template <int STEPS>
+__device__ __forceinline__ void umma_kmajor_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t bh, uint32_t idesc) {
+#pragma unroll
+    for (int kk = 0; kk < STEPS; ++kk)
+        umma_bf16_ts(d, a_tmem + kk * 8, desc(b + (((kk >> 2) * bh + (kk & 3) * 32) >> 4), kDescSw128Hi), idesc, kk > 0 ? 1u : 0u);
 }
 // D (+)= A B over K = 16 * STEPS rows of B (MN-major, 128 bytes a row and half), A in tensor memory
 template <int STEPS>
