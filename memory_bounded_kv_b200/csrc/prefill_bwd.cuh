@@ -64,7 +64,7 @@ struct DqShape {
     static constexpr int EST_OFF = LB_OFF + ST * KT * 4; // [128] estimates, [128] row sums of the second warpgroup
     static constexpr int INFO_OFF = EST_OFF + 2 * R * 4;
     static constexpr int BAR_OFF = INFO_OFF + 2 * 8 * 4;
-    static constexpr int NBAR = 4 + 3 * ST + 4 + 4;
+    static constexpr int NBAR = 4 + 3 * ST + 8 + 4;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr size_t SMEM = 1024 + MISC_OFF + 32;
     static constexpr int TM_Q = 0, TM_DO = 64, TM_S = 128, TM_DP = 256, TM_DQ = 384, TM_COLS = 512;
@@ -89,8 +89,10 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
     uint64_t* kv_full = bars + 4;
     uint64_t* kv_empty = kv_full + ST;
     uint64_t* x_full = kv_empty + ST;    // the bias columns and slopes; K's and V's rows past the document cleared
-    uint64_t* s_full = x_full + ST;      // [buffer] S and dP
-    uint64_t* ds_full = s_full + 2;
+    uint64_t* s_full = x_full + ST;      // [buffer]
+    uint64_t* s_read = s_full + 2;
+    uint64_t* dp_full = s_read + 2;
+    uint64_t* ds_full = dp_full + 2;
     uint64_t* u_full = ds_full + 2;
     uint64_t* u_empty = u_full + 2;
     int* info = reinterpret_cast<int*>(smem + SH::INFO_OFF);
@@ -113,9 +115,11 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
+            mbar_init(&s_read[t], 4);
+            mbar_init(&dp_full[t], 1);
             mbar_init(&ds_full[t], 4);
             mbar_init(&u_full[t], 1);
-            mbar_init(&u_empty[t], 10);   // products, bias, 8 softmax warps
+            mbar_init(&u_empty[t], 11);   // products, 2 bias warps, 8 softmax warps
         }
         mbar_init(fin, 1);
         *s_abort = 0;
@@ -203,8 +207,9 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 }
             }
             if (stop && lane == 0) fail();
-        } else if (warp == 10) {
+        } else if (warp >= 10) {
             // ======================= bias columns, K and V past a document's end =======================
+            // two warps, a step each in turn; the log betas of a warp's next step load while it writes this one's
             const float unit_b = CAP ? kLog2e : 1.f / p.scale;
             int step = 0;
             bool stop = false;
@@ -216,18 +221,22 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&u_empty[ub]);
                 if (s < 0) break;
-                for (int tile = n - 1; tile >= 0; --tile, ++step) {
-                    const int st = step % ST;
-                    const unsigned ph = (unsigned)(step / ST) & 1u;
-                    float b[2] = {0.f, 0.f};
-                    if (BETA) {
+                float nb[2] = {0.f, 0.f};
+                auto load = [&](int tile) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int j = tile * KT + lane + 32 * e;
-                            if (j < len) b[e] = clamp_log_beta(p.lb[(long long)(s + j) * p.lb_st + g * p.lb_sh]) * unit_b;
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = tile * KT + lane + 32 * e;
+                        nb[e] = tile >= 0 && j < len ? p.lb[(long long)(s + j) * p.lb_st + g * p.lb_sh] : 0.f;
                     }
-                    if (step >= ST && !warp_wait(&kv_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
+                };
+                const int q0 = (step + warp) & 1;   // this warp's first step of the unit
+                if (BETA) load(n - 1 - q0);
+                for (int q = q0; q < n; q += 2) {
+                    const int tile = n - 1 - q, k = step + q, st = k % ST;
+                    const unsigned ph = (unsigned)(k / ST) & 1u;
+                    const float b[2] = {clamp_log_beta(nb[0]) * unit_b, clamp_log_beta(nb[1]) * unit_b};
+                    if (BETA) load(tile - 2);
+                    if (k >= ST && !warp_wait(&kv_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
                     if (BETA) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -253,6 +262,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     if (lane == 0) mbar_arrive(&x_full[st]);
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
+                step += n;
             }
             if (stop && lane == 0) fail();
         } else if (warp == 8) {
@@ -260,17 +270,15 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
             // the warp stays together (its values are uniform); one lane issues
             constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
             int step = 0;
-            unsigned dc = 0;           // bit t: parity of buffer t's next dS
+            unsigned rd = 0, dc = 0;   // bit t: parity of buffer t's next reading of S, next dS
             bool stop = false;
             const uint32_t k_lo = desc_sw128_lo(sbase + SH::KV_OFF), kr_lo = desc_mn_lo(sbase + SH::KV_OFF, SH::KHALF);
             const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
             auto scores = [&](int t, int st, bool past) {
-                const uint32_t k = k_lo + st * (2 * SH::KTILE >> 4);
-                umma_kmajor_ts<D / 16>(tmem + SH::TM_S + t * 64, tmem + SH::TM_Q, k, SH::KHALF, idesc_s);
+                umma_kmajor_ts<D / 16>(tmem + SH::TM_S + t * 64, tmem + SH::TM_Q, k_lo + st * (2 * SH::KTILE >> 4), SH::KHALF, idesc_s);
                 if (BETA && !CAP && past)
                     umma_bf16(tmem + SH::TM_S + t * 64, desc(qx_lo, kDescPlainHi), desc(kx_lo + st * (KT * 32 >> 4), kDescPlainHi),
                               idesc_s, 1u);
-                umma_kmajor_ts<D / 16>(tmem + SH::TM_DP + t * 64, tmem + SH::TM_DO, k + (SH::KTILE >> 4), SH::KHALF, idesc_s);
                 umma_commit(&s_full[t]);
             };
             for (int uc = 0; !stop; ++uc) {
@@ -282,22 +290,40 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 if (s < 0) break;
                 if (!warp_wait(a_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
                 for (int q = 0; q < n + 2; ++q) {
-                    // step q - 2's gradient frees buffer q % 2 for step q's scores
+                    // step q's scores once step q - 2's were read from their buffer; then step q - 2's
+                    // gradient, whose dS lies in the buffer of dP, and step q's dP
                     const int k = step + q, t = q & 1, st = k % ST, dst = (k + 2 * ST - 2) % ST;
+                    if (q < n) {
+                        if (q >= 2) {
+                            if (!warp_wait(&s_read[t], (rd >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                            rd ^= 1u << t;
+                        }
+                        if (!warp_wait(&kv_full[st], (unsigned)(k / ST) & 1u, p.wait_ns) ||
+                            !warp_wait(&x_full[st], (unsigned)(k / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                        tc_fence_after();
+                        if (elect_one()) scores(t, st, (n - q) * KT <= i0 + 1);
+                        __syncwarp();
+                    }
                     if (q >= 2) {
+                        if (q >= n) {   // the readings that no further scores wait for
+                            if (!warp_wait(&s_read[t], (rd >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                            rd ^= 1u << t;
+                        }
                         if (!warp_wait(&ds_full[t], (dc >> t) & 1u, p.wait_ns)) { stop = true; break; }
                         dc ^= 1u << t;
                     }
-                    if (q < n && (!warp_wait(&kv_full[st], (unsigned)(k / ST) & 1u, p.wait_ns) ||
-                                  !warp_wait(&x_full[st], (unsigned)(k / ST) & 1u, p.wait_ns))) { stop = true; break; }
                     tc_fence_after();
                     if (elect_one()) {
                         if (q >= 2) {
-                            umma_rows<KT / 16>(tmem + SH::TM_DQ, tmem + SH::TM_S + t * 64, kr_lo + dst * (2 * SH::KTILE >> 4),
+                            umma_rows<KT / 16>(tmem + SH::TM_DQ, tmem + SH::TM_DP + t * 64, kr_lo + dst * (2 * SH::KTILE >> 4),
                                                idesc_o, q == 2);
                             umma_commit(&kv_empty[dst]);
                         }
-                        if (q < n) scores(t, st, (n - q) * KT <= i0 + 1);
+                        if (q < n) {
+                            umma_kmajor_ts<D / 16>(tmem + SH::TM_DP + t * 64, tmem + SH::TM_DO,
+                                                   k_lo + (st * 2 + 1) * (SH::KTILE >> 4), SH::KHALF, idesc_s);
+                            umma_commit(&dp_full[t]);
+                        }
                         if (q == n + 1) umma_commit(o_full);
                     }
                     __syncwarp();
@@ -390,6 +416,9 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 tmem_ld32(tl + SH::TM_S + t * 64, x);
                 tmem_ld32(tl + SH::TM_S + t * 64 + 32, x + 32);
                 tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_read[t]);
                 if (CAP) {
                     cap_tanh<64>(x, th, per_cap);
 #pragma unroll
@@ -421,6 +450,8 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     x[c + 1] = ex2_approx(v);
                 }
                 uint64_t sum = 0ull;
+                if (!warp_wait(&dp_full[t], (unsigned)sc & 1u, p.wait_ns)) { stop = true; break; }
+                tc_fence_after();
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
                     float dp[32];
@@ -439,7 +470,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                         }
                         w[e / 2] = pack_bf16(u, v);   // dS enters dS K as bf16: 2^-9 each, as dq's own rounding
                     }
-                    tmem_st16(tl + SH::TM_S + t * 64 + c0 / 2, w);
+                    tmem_st16(tl + SH::TM_DP + t * 64 + c0 / 2, w);
                 }
                 float s0, s1;
                 upk2(sum, s0, s1);
@@ -569,7 +600,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
         mbar_init(db_full, 4);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&u_full[t], 1);
-            mbar_init(&u_empty[t], 10);
+            mbar_init(&u_empty[t], 11);
         }
         mbar_init(fin, 1);
         *s_abort = 0;
@@ -669,8 +700,9 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 }
             }
             if (stop && lane == 0) fail();
-        } else if (warp == 10) {
+        } else if (warp >= 10) {
             // ======================= extra columns, row values, rows past a document's end =======================
+            // two warps, a step each in turn; the rows' numbers of a warp's next step load while it writes this one's
             int step = 0;
             bool stop = false;
             for (int uc = 0; !stop; ++uc) {
@@ -681,8 +713,24 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&u_empty[ub]);
                 if (s < 0) break;
-                const int last = j0 + KT - 1;
-                if (BETA && !CAP) {
+                const int last = j0 + KT - 1, n = b1 - b0;
+                float lse[4], delta[4];
+                auto load = [&](int blk) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = lane + 32 * e, i = blk * bt + (c >> lg);
+                        lse[e] = 1.2676506e30f;   // no such row (2^100): P = 0
+                        delta[e] = 0.f;
+                        if (i < len) {
+                            const size_t row = (size_t)(s + i) * p.Hq + (g << lg) + (c & (p.G - 1));
+                            lse[e] = p.lse[row];
+                            delta[e] = p.delta[row];
+                        }
+                    }
+                };
+                const int q0 = (step + warp) & 1;   // this warp's first step of the unit
+                load(b0 + q0);
+                if (BETA && !CAP && warp == 10 + (step & 1)) {   // the warp of the unit's first step
                     float b[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -699,35 +747,30 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         *reinterpret_cast<uint4*>(smem + SH::KX_OFF + plain16_off(c, 1)) = c1;
                     }
                 }
-                for (int blk = b0; blk < b1; ++blk, ++step) {
-                    const int st = step % ST;
-                    const unsigned ph = (unsigned)(step / ST) & 1u;
-                    float lse[4], delta[4];
+                for (int q = q0; q < n; q += 2) {
+                    const int blk = b0 + q, k = step + q, st = k % ST;
+                    const unsigned ph = (unsigned)(k / ST) & 1u;
+                    float y[4], dl[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int c = lane + 32 * e, i = blk * bt + (c >> lg);
-                        lse[e] = 1.2676506e30f;   // no such row (2^100): P = 0
-                        delta[e] = 0.f;
-                        if (i < len) {
-                            const size_t row = (size_t)(s + i) * p.Hq + (g << lg) + (c & (p.G - 1));
-                            lse[e] = p.lse[row];
-                            delta[e] = p.delta[row];
-                        }
+                        y[e] = lse[e] * (CAP ? kLog2e : -1.f / p.scale);
+                        dl[e] = -delta[e];
                     }
-                    if (step >= ST && !warp_wait(&q_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
+                    load(blk + 2);
+                    if (k >= ST && !warp_wait(&q_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int c = lane + 32 * e;
                         uint4 c0, c1;
                         unsigned char* at = smem + SH::QX_OFF + st * 2 * QT * 32;
                         if (CAP) {
-                            reinterpret_cast<float*>(smem + SH::ROW_OFF)[st * QT + c] = lse[e] * kLog2e;
+                            reinterpret_cast<float*>(smem + SH::ROW_OFF)[st * QT + c] = y[e];
                         } else {
-                            far_query(BETA ? max(blk * bt + (c >> lg) - last, 0) : 0, lse[e] * (-1.f / p.scale), c0, c1);
+                            far_query(BETA ? max(blk * bt + (c >> lg) - last, 0) : 0, y[e], c0, c1);
                             *reinterpret_cast<uint4*>(at + plain16_off(c, 0)) = c0;
                             *reinterpret_cast<uint4*>(at + plain16_off(c, 1)) = c1;
                         }
-                        far_query(0, -delta[e], c0, c1);
+                        far_query(0, dl[e], c0, c1);
                         *reinterpret_cast<uint4*>(at + QT * 32 + plain16_off(c, 0)) = c0;
                         *reinterpret_cast<uint4*>(at + QT * 32 + plain16_off(c, 1)) = c1;
                     }
@@ -746,6 +789,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     if (lane == 0) mbar_arrive(&x_full[st]);
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
+                step += n;
             }
             if (stop && lane == 0) fail();
         } else if (warp == 8) {
@@ -919,9 +963,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 // ---- dS
                 if (!warp_wait(dp_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
-                // d log beta: where all is past, sum dS (di + tok(c)) with tok(c) = c >> lg, from the eight
-                // sums over c = e mod 8 and from sum (c / 8) dS; else the distances one by one
-                uint64_t by8[4] = {0ull, 0ull, 0ull, 0ull}, up = 0ull;
+                uint64_t ds[32];
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
                     float dp[32];
@@ -930,18 +972,10 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const uint64_t ds = mul2(pk2(x[c0 + e], x[c0 + e + 1]), pk2(dp[e], dp[e + 1]));
-                        if (BETA) {
-                            if (past) {
-                                by8[(e / 2) & 3] = add2(by8[(e / 2) & 3], ds);
-                                up = fma2(ds, pk2((float)((c0 + e) / 8), (float)((c0 + e) / 8)), up);
-                            } else {
-                                const float2 k2 = reinterpret_cast<const float2*>(tok4)[(c0 + e) / 2];
-                                up = fma2(ds, pk2(fmaxf(di + k2.x, 0.f), fmaxf(di + k2.y, 0.f)), up);
-                            }
-                        }
+                        const uint64_t d = mul2(pk2(x[c0 + e], x[c0 + e + 1]), pk2(dp[e], dp[e + 1]));
+                        ds[(c0 + e) / 2] = d;
                         float a, b;
-                        upk2(ds, a, b);
+                        upk2(d, a, b);
                         if (CAP) {
                             a *= 1.f - th[c0 + e] * th[c0 + e];
                             b *= 1.f - th[c0 + e + 1] * th[c0 + e + 1];
@@ -954,11 +988,23 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ds_full);
+                // ---- d log beta, while the products run. Where all is past: sum dS (di + tok(c)), tok(c) =
+                // c >> lg, from the eight sums over c = e mod 8 and from sum (c / 8) dS; else one by one
                 if (BETA) {
-                    float u0, u1;
-                    upk2(up, u0, u1);
                     if (past) {
-                        float part = (u0 + u1) * (float)(8 >> lg), all = 0.f;
+                        uint64_t by8[4], up = 0ull;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) by8[e] = ds[e];
+#pragma unroll
+                        for (int c = 4; c < 32; c += 4) {
+                            uint64_t four = add2(add2(ds[c], ds[c + 1]), add2(ds[c + 2], ds[c + 3]));
+                            up = fma2(four, same2((float)(c / 4)), up);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) by8[e] = add2(by8[e], ds[c + e]);
+                        }
+                        float u0, u1, all = 0.f;
+                        upk2(up, u0, u1);
+                        float part = (u0 + u1) * (float)(8 >> lg);
 #pragma unroll
                         for (int e = 0; e < 8; e += 2) {
                             float a, b;
@@ -969,7 +1015,16 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         }
                         db += fmaf(all, di, part);
                     } else {
-                        db += u0 + u1;
+                        float u = 0.f, v = 0.f;
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            const float2 k2 = reinterpret_cast<const float2*>(tok4)[c / 2];
+                            float a, b;
+                            upk2(ds[c / 2], a, b);
+                            u = fmaf(a, fmaxf(di + k2.x, 0.f), u);
+                            v = fmaf(b, fmaxf(di + k2.y, 0.f), v);
+                        }
+                        db += u + v;
                     }
                 }
             }

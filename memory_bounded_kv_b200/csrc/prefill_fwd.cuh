@@ -19,7 +19,7 @@
 //
 // Roles (384 threads, one CTA per SM, persistent): warps 0-3 and 4-7 softmax and output of tiles 0
 // and 1 (a thread per row), warp 8 issues the products, warp 9 finds the units and issues the TMA
-// loads, warp 10 writes the bias columns and clears V's rows past a document's end (their P is 0,
+// loads, warps 10 and 11 write the bias columns and clear V's rows past a document's end (their P is 0,
 // but 0 times a neighbour's NaN is not).
 // Every wait is bounded (wait_ns); a CTA that gives up records KVB_DERR_TIMEOUT and lets its copies
 // and products finish (bounded); the rows that it had not written keep what they held.
@@ -33,7 +33,7 @@ template <int D>
 struct FwdShape {
     static constexpr int R = 128, KT = 128;              // rows of a query tile, keys of a key tile
     static constexpr int ST = D == 128 ? 2 : 4;          // K and V ring stages
-    static constexpr int NT = 12 * 32;                  // three warpgroups (warp 11 idles)
+    static constexpr int NT = 12 * 32;
     static constexpr int REG_SOFT = 208, REG_REST = 88;  // 2 x 208 + 88 = 3 x 168, the launch's registers
     static constexpr int HALF = 128 * 128;               // 128 rows x 64 dims of bf16
     static constexpr int TILE = HALF * (D / 64);
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
             mbar_init(&o_full[t], 1);
             mbar_init(&o_empty[t], 4);
             mbar_init(&u_full[t], 1);
-            mbar_init(&u_empty[t], 10);   // products, bias, 8 softmax warps
+            mbar_init(&u_empty[t], 11);   // products, 2 bias warps, 8 softmax warps
         }
         mbar_init(fin, 1);
         *s_abort = 0;
@@ -221,38 +221,47 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
             }
             if (stop && lane == 0) fail();
         }
-    } else if (warp == 10) {
+    } else if (warp >= 10) {
         // ======================= bias columns, V past a document's end =======================
+        // two warps, a step each in turn; the log betas of a warp's next step load while it writes this one's
         const float unit_b = CAP ? kLog2e : 1.f / p.scale;
         int step = 0;
         bool stop = false;
         for (int uc = 0; !stop; ++uc) {
             const int ub = uc & 1;
-            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) break;
+            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
             const int* m = info + ub * 8;
             const int s = m[0], len = m[1], i0 = m[2], g = m[3], n = max(m[5], m[6]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&u_empty[ub]);
             if (s < 0) break;
-            for (int tile = n - 1; tile >= 0; --tile, ++step) {
-                const int st = step % ST;
-                const unsigned ph = (unsigned)(step / ST) & 1u;
+            float nb[4] = {0.f, 0.f, 0.f, 0.f};
+            auto load = [&](int tile) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = tile * KT + lane + 32 * e;
+                    nb[e] = tile >= 0 && j < len ? p.lb[(long long)(s + j) * p.lb_st + g * p.lb_sh] : 0.f;
+                }
+            };
+            const int q0 = (step + warp) & 1;   // this warp's first step of the unit
+            if (BETA) load(n - 1 - q0);
+            for (int q = q0; q < n; q += 2) {
+                const int tile = n - 1 - q, k = step + q, st = k % ST;
+                const unsigned ph = (unsigned)(k / ST) & 1u;
                 if (BETA) {
                     float b[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = tile * KT + lane + 32 * e;
-                        b[e] = j < len ? clamp_log_beta(p.lb[(long long)(s + j) * p.lb_st + g * p.lb_sh]) * unit_b : 0.f;
-                    }
-                    // the slopes of step - ST were read before its P V product, which freed the V stage
-                    if (step >= ST && !warp_wait(&v_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
+                    for (int e = 0; e < 4; ++e) b[e] = clamp_log_beta(nb[e]) * unit_b;
+                    load(tile - 2);
+                    // the slopes of step k - ST were read before its P V product, which freed the V stage
+                    if (k >= ST && !warp_wait(&v_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         reinterpret_cast<float*>(smem + SH::LB_OFF)[st * KT + lane + 32 * e] = b[e];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&lb_full[st]);
                     if (!CAP) {
-                        if (step >= ST && !warp_wait(&k_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
+                        if (k >= ST && !warp_wait(&k_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int c = lane + 32 * e;
@@ -279,6 +288,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                 }
                 if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
             }
+            step += n;
         }
         if (stop && lane == 0) fail();
     } else if (warp == 8) {
