@@ -16,12 +16,13 @@
 // shared-memory operands reads 16 (128 + N) x 2 bytes per K step of 16: at N = 64 that is 48 clocks of
 // the 128 bytes a clock for 32 clocks of mathematics, at N = 128 it is 64 for 64 (measured: 48.8 and
 // 64.4 clocks a step; with the first operand in tensor memory 32.7 and 63.4).
-//   By query rows, the block's Q and dO live in tensor memory (written there once per unit), so that
-// steps of 64 keys cost no more than their mathematics; two S and dP pairs are in flight, one per
-// warpgroup: while it turns its pair into dS, the products of the other run.
-//   By keys there is no room for that (dK, dV, S and dP fill the tensor memory), so steps take 128 query
-// rows. S and dP alternate: P done -> dV += P^T dO and the next S, while the warpgroups turn dP into dS;
-// dS done -> dK += dS^T Q and the next dP, while they turn the next S into P.
+//   By query rows, the block's Q and dO live in tensor memory (written there once per unit), so that S
+// and dP leave shared memory to the copies. The next S is issued as soon as the warpgroups have read one;
+// dS goes over dP, so dQ += dS K comes before the next dP, which the exponentials hide.
+//   By keys there is no room for that (dK, dV, S and dP fill the tensor memory). S and dP alternate:
+// P done -> dV += P^T dO and the next S, while the warpgroups turn dP into dS; dS done -> dK += dS^T Q
+// and the next dP, while they turn the next S into P.
+//   The two warpgroups share a tile: each takes 64 of its 128 columns, a thread per row.
 // The bias rides the S product as in prefill_fwd_kernel; by keys, - lse and - delta ride S and dP too.
 #pragma once
 
@@ -52,8 +53,8 @@ __device__ __forceinline__ void far_key(float b, int last_minus_j, uint4& c0, ui
 
 template <int D>
 struct DqShape {
-    static constexpr int R = 128, KT = 64;
-    static constexpr int ST = D == 128 ? 5 : 8;          // K/V ring stages
+    static constexpr int R = 128, KT = 128;
+    static constexpr int ST = D == 128 ? 3 : 6;          // K/V ring stages
     static constexpr int NT = 12 * 32;
     static constexpr int REG_SOFT = 208, REG_REST = 88;  // 2 x 208 + 88 = 3 x 168, the launch's registers
     static constexpr int KHALF = KT * 128, KTILE = KHALF * (D / 64);
@@ -64,7 +65,7 @@ struct DqShape {
     static constexpr int EST_OFF = LB_OFF + ST * KT * 4; // [128] estimates, [128] row sums of the second warpgroup
     static constexpr int INFO_OFF = EST_OFF + 2 * R * 4;
     static constexpr int BAR_OFF = INFO_OFF + 2 * 8 * 4;
-    static constexpr int NBAR = 4 + 3 * ST + 8 + 4;
+    static constexpr int NBAR = 4 + 3 * ST + 4 + 4;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr size_t SMEM = 1024 + MISC_OFF + 32;
     static constexpr int TM_Q = 0, TM_DO = 64, TM_S = 128, TM_DP = 256, TM_DQ = 384, TM_COLS = 512;
@@ -89,11 +90,11 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
     uint64_t* kv_full = bars + 4;
     uint64_t* kv_empty = kv_full + ST;
     uint64_t* x_full = kv_empty + ST;    // the bias columns and slopes; K's and V's rows past the document cleared
-    uint64_t* s_full = x_full + ST;      // [buffer]
-    uint64_t* s_read = s_full + 2;
-    uint64_t* dp_full = s_read + 2;
-    uint64_t* ds_full = dp_full + 2;
-    uint64_t* u_full = ds_full + 2;
+    uint64_t* s_full = x_full + ST;
+    uint64_t* s_read = s_full + 1;
+    uint64_t* dp_full = s_full + 2;
+    uint64_t* ds_full = s_full + 3;
+    uint64_t* u_full = s_full + 4;
     uint64_t* u_empty = u_full + 2;
     int* info = reinterpret_cast<int*>(smem + SH::INFO_OFF);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + SH::MISC_OFF);
@@ -113,13 +114,13 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
             mbar_init(&kv_empty[s], 1);
             mbar_init(&x_full[s], 1);
         }
+        mbar_init(s_full, 1);
+        mbar_init(s_read, 8);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, 8);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&s_full[t], 1);
-            mbar_init(&s_read[t], 4);
-            mbar_init(&dp_full[t], 1);
-            mbar_init(&ds_full[t], 4);
             mbar_init(&u_full[t], 1);
-            mbar_init(&u_empty[t], 11);   // products, 2 bias warps, 8 softmax warps
+            mbar_init(&u_empty[t], 10);   // products, bias, 8 softmax warps
         }
         mbar_init(fin, 1);
         *s_abort = 0;
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
             *reinterpret_cast<uint4*>(smem + SH::QX_OFF + plain16_off(x, 1)) = make_uint4(0u, 0u, 0u, 0u);
         }
         for (int x = tid; x < ST * KT; x += SH::NT)
-            *reinterpret_cast<uint4*>(smem + SH::KX_OFF + (x >> 6) * KT * 32 + plain16_off(x & 63, 1)) =
+            *reinterpret_cast<uint4*>(smem + SH::KX_OFF + (x >> 7) * KT * 32 + plain16_off(x & 127, 1)) =
                 make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
@@ -207,9 +208,9 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 }
             }
             if (stop && lane == 0) fail();
-        } else if (warp >= 10) {
+        } else if (warp == 10) {
             // ======================= bias columns, K and V past a document's end =======================
-            // two warps, a step each in turn; the log betas of a warp's next step load while it writes this one's
+            // the log betas of the next step load while it writes this one's
             const float unit_b = CAP ? kLog2e : 1.f / p.scale;
             int step = 0;
             bool stop = false;
@@ -221,25 +222,26 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&u_empty[ub]);
                 if (s < 0) break;
-                float nb[2] = {0.f, 0.f};
+                float nb[4] = {0.f, 0.f, 0.f, 0.f};
                 auto load = [&](int tile) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const int j = tile * KT + lane + 32 * e;
                         nb[e] = tile >= 0 && j < len ? p.lb[(long long)(s + j) * p.lb_st + g * p.lb_sh] : 0.f;
                     }
                 };
-                const int q0 = (step + warp) & 1;   // this warp's first step of the unit
-                if (BETA) load(n - 1 - q0);
-                for (int q = q0; q < n; q += 2) {
+                if (BETA) load(n - 1);
+                for (int q = 0; q < n; ++q) {
                     const int tile = n - 1 - q, k = step + q, st = k % ST;
                     const unsigned ph = (unsigned)(k / ST) & 1u;
-                    const float b[2] = {clamp_log_beta(nb[0]) * unit_b, clamp_log_beta(nb[1]) * unit_b};
-                    if (BETA) load(tile - 2);
+                    float b[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) b[e] = clamp_log_beta(nb[e]) * unit_b;
+                    if (BETA) load(tile - 1);
                     if (k >= ST && !warp_wait(&kv_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
                     if (BETA) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int e = 0; e < 4; ++e) {
                             const int c = lane + 32 * e;
                             reinterpret_cast<float*>(smem + SH::LB_OFF)[st * KT + c] = b[e];
                             if (!CAP)
@@ -270,16 +272,22 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
             // the warp stays together (its values are uniform); one lane issues
             constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
             int step = 0;
-            unsigned rd = 0, dc = 0;   // bit t: parity of buffer t's next reading of S, next dS
             bool stop = false;
             const uint32_t k_lo = desc_sw128_lo(sbase + SH::KV_OFF), kr_lo = desc_mn_lo(sbase + SH::KV_OFF, SH::KHALF);
             const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
-            auto scores = [&](int t, int st, bool past) {
-                umma_kmajor_ts<D / 16>(tmem + SH::TM_S + t * 64, tmem + SH::TM_Q, k_lo + st * (2 * SH::KTILE >> 4), SH::KHALF, idesc_s);
+            auto scores = [&](int st, bool past) {
+                umma_kmajor_ts<D / 16>(tmem + SH::TM_S, tmem + SH::TM_Q, k_lo + st * (2 * SH::KTILE >> 4), SH::KHALF, idesc_s);
                 if (BETA && !CAP && past)
-                    umma_bf16(tmem + SH::TM_S + t * 64, desc(qx_lo, kDescPlainHi), desc(kx_lo + st * (KT * 32 >> 4), kDescPlainHi),
-                              idesc_s, 1u);
-                umma_commit(&s_full[t]);
+                    umma_bf16(tmem + SH::TM_S, desc(qx_lo, kDescPlainHi), desc(kx_lo + st * (KT * 32 >> 4), kDescPlainHi), idesc_s, 1u);
+                umma_commit(s_full);
+            };
+            auto pulls = [&](int st) {
+                umma_kmajor_ts<D / 16>(tmem + SH::TM_DP, tmem + SH::TM_DO, k_lo + (st * 2 + 1) * (SH::KTILE >> 4), SH::KHALF, idesc_s);
+                umma_commit(dp_full);
+            };
+            auto loaded = [&](int k) {
+                return warp_wait(&kv_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns) &&
+                       warp_wait(&x_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns);
             };
             for (int uc = 0; !stop; ++uc) {
                 const int ub = uc & 1;
@@ -288,48 +296,38 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 const int s = __shfl_sync(kFull, m[0], 0), i0 = __shfl_sync(kFull, m[2], 0), n = __shfl_sync(kFull, m[5], 0);
                 if (lane == 0) mbar_arrive(&u_empty[ub]);
                 if (s < 0) break;
-                if (!warp_wait(a_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
-                for (int q = 0; q < n + 2; ++q) {
-                    // step q's scores once step q - 2's were read from their buffer; then step q - 2's
-                    // gradient, whose dS lies in the buffer of dP, and step q's dP
-                    const int k = step + q, t = q & 1, st = k % ST, dst = (k + 2 * ST - 2) % ST;
-                    if (q < n) {
-                        if (q >= 2) {
-                            if (!warp_wait(&s_read[t], (rd >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                            rd ^= 1u << t;
-                        }
-                        if (!warp_wait(&kv_full[st], (unsigned)(k / ST) & 1u, p.wait_ns) ||
-                            !warp_wait(&x_full[st], (unsigned)(k / ST) & 1u, p.wait_ns)) { stop = true; break; }
-                        tc_fence_after();
-                        if (elect_one()) scores(t, st, (n - q) * KT <= i0 + 1);
-                        __syncwarp();
-                    }
-                    if (q >= 2) {
-                        if (q >= n) {   // the readings that no further scores wait for
-                            if (!warp_wait(&s_read[t], (rd >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                            rd ^= 1u << t;
-                        }
-                        if (!warp_wait(&ds_full[t], (dc >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                        dc ^= 1u << t;
-                    }
+                if (!warp_wait(a_full, (unsigned)uc & 1u, p.wait_ns) || !loaded(step)) { stop = true; break; }
+                tc_fence_after();
+                if (elect_one()) {
+                    scores(step % ST, n * KT <= i0 + 1);
+                    pulls(step % ST);
+                }
+                __syncwarp();
+                for (int tile = n - 1; tile >= 0; --tile, ++step) {
+                    const int st = step % ST, nst = (step + 1) % ST;
+                    const bool more = tile > 0;
+                    // the next scores as soon as these are read
+                    if (more && !loaded(step + 1)) { stop = true; break; }
+                    if (!warp_wait(s_read, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
+                    tc_fence_after();
+                    if (elect_one() && more) scores(nst, tile * KT <= i0 + 1);
+                    __syncwarp();
+                    if (!warp_wait(ds_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                     tc_fence_after();
                     if (elect_one()) {
-                        if (q >= 2) {
-                            umma_rows<KT / 16>(tmem + SH::TM_DQ, tmem + SH::TM_DP + t * 64, kr_lo + dst * (2 * SH::KTILE >> 4),
-                                               idesc_o, q == 2);
-                            umma_commit(&kv_empty[dst]);
+                        // dS: a warpgroup's 64 columns as 32 words at the start of its half of dP
+                        const uint32_t b = kr_lo + st * (2 * SH::KTILE >> 4);
+                        umma_rows<4>(tmem + SH::TM_DQ, tmem + SH::TM_DP, b, idesc_o, tile == n - 1);
+                        umma_rows<4>(tmem + SH::TM_DQ, tmem + SH::TM_DP + 64, b + 64 * 128 / 16, idesc_o, false);
+                        umma_commit(&kv_empty[st]);
+                        if (more) {
+                            pulls(nst);
+                        } else {
+                            umma_commit(o_full);
                         }
-                        if (q < n) {
-                            umma_kmajor_ts<D / 16>(tmem + SH::TM_DP + t * 64, tmem + SH::TM_DO,
-                                                   k_lo + (st * 2 + 1) * (SH::KTILE >> 4), SH::KHALF, idesc_s);
-                            umma_commit(&dp_full[t]);
-                        }
-                        if (q == n + 1) umma_commit(o_full);
                     }
                     __syncwarp();
                 }
-                if (stop) break;
-                step += n;
             }
             if (stop && lane == 0) fail();
         }
@@ -343,7 +341,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
         const float cap2 = CAP ? p.softcap * kLog2e : 0.f, per_cap = CAP ? p.scale / p.softcap : 0.f;
         float* s_est = reinterpret_cast<float*>(smem + SH::EST_OFF);
         float* s_sum = s_est + R;
-        int sc = 0, step = 0;
+        int step = 0;
         bool stop = false;
         int s = -1, len = 0, i0 = 0, g = 0, pre = 0, n = 0;
         uint32_t a[D / 2];
@@ -408,9 +406,9 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 est = s_est[r];
             }
             float rsum = 0.f;
-            for (int q = t; q < n; q += 2, ++sc) {
-                const int k = step + q, st = k % ST, j0 = (n - 1 - q) * KT;
-                if (!warp_wait(&s_full[t], (unsigned)sc & 1u, p.wait_ns)) { stop = true; break; }
+            for (int tile = n - 1; tile >= 0; --tile, ++step) {
+                const int st = step % ST, j0 = tile * KT + 64 * t;   // this warpgroup's keys
+                if (!warp_wait(s_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
                 float x[64], th[CAP ? 64 : 1];
                 tmem_ld32(tl + SH::TM_S + t * 64, x);
@@ -418,15 +416,15 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s_read[t]);
+                if (lane == 0) mbar_arrive(s_read);
                 if (CAP) {
                     cap_tanh<64>(x, th, per_cap);
 #pragma unroll
                     for (int c = 0; c < 64; ++c) x[c] = cap2 * th[c];
                 }
-                if (BETA && (CAP || j0 + KT > first + 1)) {
-                    if (!warp_wait(&x_full[st], (unsigned)(k / ST) & 1u, p.wait_ns)) { stop = true; break; }
-                    const float4* lb = reinterpret_cast<const float4*>(smem + SH::LB_OFF + st * KT * 4);
+                if (BETA && (CAP || (tile + 1) * KT > first + 1)) {
+                    if (!warp_wait(&x_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                    const float4* lb = reinterpret_cast<const float4*>(smem + SH::LB_OFF + (st * KT + 64 * t) * 4);
                     const float di = (float)(i - j0);
 #pragma unroll
                     for (int c = 0; c < 64; c += 4) {
@@ -437,7 +435,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                         x[c + 3] = fmaf(fmaxf(di - (c + 3), 0.f), b.w, x[c + 3]);
                     }
                 }
-                if (j0 + KT > max(first + 1, pre)) {
+                if (j0 + 64 > max(first + 1, pre)) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) x[c] = c < lim - j0 ? x[c] : -INFINITY;
                 }
@@ -446,11 +444,17 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 for (int c = 0; c < 64; c += 2) {
                     float u, v;
                     upk2(fma2(pk2(x[c], x[c + 1]), c2, n2), u, v);
-                    x[c] = ex2_approx(u);
-                    x[c + 1] = ex2_approx(v);
+                    if (c % 8 == 6) {   // a quarter of the exponentials on the FMA pipe
+                        exp2_poly2<5>(u, v);
+                    } else {
+                        u = ex2_approx(u);
+                        v = ex2_approx(v);
+                    }
+                    x[c] = u;
+                    x[c + 1] = v;
                 }
                 uint64_t sum = 0ull;
-                if (!warp_wait(&dp_full[t], (unsigned)sc & 1u, p.wait_ns)) { stop = true; break; }
+                if (!warp_wait(dp_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
@@ -478,10 +482,9 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ds_full[t]);
+                if (lane == 0) mbar_arrive(ds_full);
             }
             if (stop) break;
-            step += n;
             if (t == 1) {
                 // the first warpgroup has begun this unit, so it has read the last one's sums
                 if (!warp_wait(a_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
