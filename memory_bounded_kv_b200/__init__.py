@@ -651,74 +651,106 @@ def kvb_paged_compact_blocks(pool, rm_start, rm_len, *, stream=None) -> None:
 # prompts: attention over packed documents, its gradients, and whole prompts into a paged cache
 # ----------------------------------------------------------------------------------------------
 
-def _one_device(tensors):
-    """The device that all of {name: tensor or None} are on (CUDA); ValueError when they differ."""
-    dev = None
-    for name, x in tensors.items():
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _is(x, dtype, shape, name, contiguous=True):
+    """Raise unless x is a tensor of `dtype` and `shape` (and contiguous). Devices are checked later."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+    if contiguous and not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _one_device(*tensors):
+    """The index of the CUDA device that all the tensors (those not None) are on."""
+    dev = tensors[0].get_device()
+    for x in tensors:
         if x is None:
             continue
-        if not x.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if dev is not None and x.device != dev:
-            raise ValueError(f"{name} is on {x.device}, the other tensors on {dev}")
-        dev = x.device
+        d = x.get_device()
+        if d < 0:
+            raise TypeError("every tensor must be a CUDA tensor")
+        if d != dev:
+            raise ValueError(f"tensors on different devices: cuda:{dev} and cuda:{d}")
     return dev
 
 
-def _launch(device, stream, call, where):
-    """call(stream) with `device` current (the library launches on the current device)."""
-    with torch.cuda.device(device):
-        _check(call(_stream(stream)), where)
+def _launch(dev, stream, where, call, *args):
+    """call(*args, stream) with device `dev` current (the library launches on the current device)."""
+    if stream is None:
+        s = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    else:
+        s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if dev == torch.cuda.current_device():
+        status = call(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, s)
+    if status != _lib.KVB_OK:
+        raise KvbError(status, where)
 
 
-def _packed_strides(x, T, H, name):
+def _packed_strides(x, T, H, d, name):
     """(token, head) strides of a packed [T, H, d] tensor; those of a dimension of size 1 do not matter."""
-    d = x.shape[2]
-    if x.stride(2) != 1:
+    st, sh, sd = x.stride()
+    if sd != 1:
         raise ValueError(f"{name}: innermost dim must be contiguous")
-    sh = x.stride(1) if H > 1 else d
-    st = x.stride(0) if T > 1 else H * d
-    return st, sh
+    return (st if T > 1 else H * d), (sh if H > 1 else d)
 
 
-def _f32_strides(x, T, H):
-    return (x.stride(0) if T > 1 else 0, x.stride(1) if H > 1 else 0)
-
-
-def _prefill_args(q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap):
-    """Checks and marshals the arguments shared by kvb_prefill_attn and kvb_prefill_attn_bwd."""
-    for name, x in (("q", q), ("k", k), ("v", v), ("cu", cu)):
-        if not isinstance(x, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-    if q.dim() != 3 or k.dim() != 3 or cu.dim() != 1 or cu.numel() < 1:
-        raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d], cu [N + 1]")
-    T, Hq, d = (int(x) for x in q.shape)
-    Hkv, N = int(k.shape[1]), cu.numel() - 1
-    for name, x, shp in (("k", k, (T, Hkv, d)), ("v", v, (T, Hkv, d)), ("log_beta", log_beta, (T, Hkv)),
-                         ("prefix_len", prefix_len, (N,)), ("o", o, (T, Hq, d)), ("lse", lse, (T, Hq))):
-        _shape(x, shp, name)
-    for name, x in (("q", q), ("k", k), ("v", v), ("o", o)):
-        _need(x, torch.bfloat16, name, cuda=False)
-    for name, x in (("log_beta", log_beta), ("lse", lse)):
-        if x is not None:
-            _need(x, torch.float32, name, cuda=False)
-    for name, x in (("cu", cu), ("prefix_len", prefix_len)):
-        if x is not None:
-            _need(x, torch.int32, name, cuda=False); _contig(x, name)
-    _contig(o, "o")
-    if lse is not None:
-        _contig(lse, "lse")
-    qs, ks, vs = (_packed_strides(x, T, H, n) for x, H, n in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v")))
+def _kv_strides(k, v, T, H, d):
+    ks, vs = _packed_strides(k, T, H, d, "k"), _packed_strides(v, T, H, d, "v")
     if ks != vs:
         raise ValueError("k and v need equal strides")
-    ls = (0, 0) if log_beta is None else _f32_strides(log_beta, T, Hkv)
-    dev = _one_device(dict(q=q, k=k, v=v, log_beta=log_beta, cu=cu, prefix_len=prefix_len, o=o, lse=lse))
-    return dev, _lib.PrefillArgs(
-        q=q.data_ptr() or None, q_stride_t=qs[0], q_stride_h=qs[1], k=k.data_ptr() or None, v=v.data_ptr() or None, kv_stride_t=ks[0],
-        kv_stride_h=ks[1], log_beta=None if log_beta is None else log_beta.data_ptr(), lb_stride_t=ls[0],
-        lb_stride_h=ls[1], cu=cu.data_ptr(), prefix_len=None if prefix_len is None else prefix_len.data_ptr(),
-        T=T, N=N, Hq=Hq, Hkv=Hkv, d=d, scale=float(scale), softcap=float(softcap), o=o.data_ptr() or None,
-        lse=None if lse is None else lse.data_ptr())
+    return ks
+
+
+def _lb_strides(log_beta, T, H):
+    if log_beta is None:
+        return 0, 0
+    st, sh = log_beta.stride()
+    return (st if T > 1 else 0), (sh if H > 1 else 0)
+
+
+def _prefill_shapes(q, k, cu):
+    for name, x, n in (("q", q, 3), ("k", k, 3), ("cu", cu, 1)):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if x.dim() != n:
+            raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d], cu [N + 1]")
+    if cu.shape[0] < 1:
+        raise ValueError("cu must be [N + 1]")
+    T, Hq, d = q.shape
+    return T, Hq, k.shape[1], d, cu.shape[0] - 1
+
+
+def _prefill_args(sizes, q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap):
+    """Checks the arguments shared by kvb_prefill_attn and kvb_prefill_attn_bwd; a packed kvb_prefill_args."""
+    T, Hq, Hkv, d, N = sizes
+    _is(q, _BF16, (T, Hq, d), "q", False)
+    _is(k, _BF16, (T, Hkv, d), "k", False)
+    _is(v, _BF16, (T, Hkv, d), "v", False)
+    _is(o, _BF16, (T, Hq, d), "o")
+    _is(cu, _I32, (N + 1,), "cu")
+    if log_beta is not None:
+        _is(log_beta, _F32, (T, Hkv), "log_beta", False)
+    if lse is not None:
+        _is(lse, _F32, (T, Hq), "lse")
+    if prefix_len is not None:
+        _is(prefix_len, _I32, (N,), "prefix_len")
+    qt, qh = _packed_strides(q, T, Hq, d, "q")
+    kt, kh = _kv_strides(k, v, T, Hkv, d)
+    lt, lh = _lb_strides(log_beta, T, Hkv)
+    return _lib.PREFILL_ARGS.pack(
+        q.data_ptr(), qt, qh, k.data_ptr(), v.data_ptr(), kt, kh, 0 if log_beta is None else log_beta.data_ptr(), lt, lh,
+        cu.data_ptr(), 0 if prefix_len is None else prefix_len.data_ptr(), T, N, Hq, Hkv, d, scale, softcap,
+        o.data_ptr(), 0 if lse is None else lse.data_ptr())
 
 
 def kvb_prefill_attn(q, k, v, log_beta, cu, o, lse=None, *, prefix_len=None, scale: float = 0.0,
@@ -730,10 +762,11 @@ def kvb_prefill_attn(q, k, v, log_beta, cu, o, lse=None, *, prefix_len=None, sca
     [T, Hq] f32 (or None) are written at the documents' rows; prefix_len [N] int32 or None: the
     first tokens of a document that every one of its rows sees; softcap 0 or the tanh cap of the
     scores; scale 0 for 1/sqrt(d)."""
-    dev, a = _prefill_args(q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap)
-    if a.T == 0 or a.N == 0:
-        return
-    _launch(dev, stream, lambda s: _lib.lib().kvb_prefill_attn(ctypes.byref(a), s), "kvb_prefill_attn")
+    sizes = _prefill_shapes(q, k, cu)
+    a = _prefill_args(sizes, q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap)
+    dev = _one_device(q, k, v, log_beta, cu, prefix_len, o, lse)
+    if sizes[0] and sizes[4]:
+        _launch(dev, stream, "kvb_prefill_attn", _lib.lib().kvb_prefill_attn, a)
 
 
 def kvb_prefill_attn_bwd_workspace_bytes(T: int, Hq: int) -> int:
@@ -751,38 +784,38 @@ def kvb_prefill_attn_bwd(q, k, v, log_beta, cu, o, lse, d_o, d_lse, dq, dk, dv, 
         raise ValueError("the gradients need lse")
     if (log_beta is None) != (d_log_beta is None):
         raise ValueError("d_log_beta is needed exactly when log_beta is given")
-    for name, x in (("q", q), ("k", k)):
-        if not isinstance(x, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if x.dim() != 3:
-            raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d]")
-    (T, Hq, d), Hkv = q.shape, k.shape[1]
-    grads = dict(d_o=d_o, d_lse=d_lse, dq=dq, dk=dk, dv=dv, d_log_beta=d_log_beta)
-    for name, shp in (("d_o", (T, Hq, d)), ("d_lse", (T, Hq)), ("dq", (T, Hq, d)), ("dk", (T, Hkv, d)),
-                      ("dv", (T, Hkv, d)), ("d_log_beta", (T, Hkv))):
-        x = grads[name]
-        if x is None and name not in ("d_lse", "d_log_beta"):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        _shape(x, shp, name)
-    for name, x in grads.items():
-        if x is not None:
-            _need(x, torch.float32 if name in ("d_lse", "d_log_beta") else torch.bfloat16, name, cuda=False); _contig(x, name)
-    _need(workspace, torch.uint8, "workspace", cuda=False); _contig(workspace, "workspace")
-    dev, a = _prefill_args(q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap)
-    _one_device(dict(q=q, workspace=workspace, **grads))
-    if a.T == 0 or a.N == 0:
-        return
-    ptr = {name: None if x is None else x.data_ptr() for name, x in grads.items()}
-    g = _lib.PrefillGrads(workspace=workspace.data_ptr(), workspace_bytes=workspace.numel(), **ptr)
-    _launch(dev, stream, lambda s: _lib.lib().kvb_prefill_attn_bwd(ctypes.byref(a), ctypes.byref(g), s),
-            "kvb_prefill_attn_bwd")
+    sizes = T, Hq, Hkv, d, N = _prefill_shapes(q, k, cu)
+    _is(d_o, _BF16, (T, Hq, d), "d_o")
+    _is(dq, _BF16, (T, Hq, d), "dq")
+    _is(dk, _BF16, (T, Hkv, d), "dk")
+    _is(dv, _BF16, (T, Hkv, d), "dv")
+    if d_lse is not None:
+        _is(d_lse, _F32, (T, Hq), "d_lse")
+    if d_log_beta is not None:
+        _is(d_log_beta, _F32, (T, Hkv), "d_log_beta")
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    _is(workspace, _U8, workspace.shape, "workspace")
+    a = _prefill_args(sizes, q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap)
+    dev = _one_device(q, k, v, log_beta, cu, prefix_len, o, lse, d_o, d_lse, dq, dk, dv, d_log_beta, workspace)
+    if T and N:
+        g = _lib.PREFILL_GRADS.pack(
+            d_o.data_ptr(), 0 if d_lse is None else d_lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            0 if d_log_beta is None else d_log_beta.data_ptr(), workspace.data_ptr(), workspace.numel())
+        _launch(dev, stream, "kvb_prefill_attn_bwd", _lib.lib().kvb_prefill_attn_bwd, a, g)
 
 
 def _pool_tensors(pool):
     if not isinstance(pool, PagedPool):
         raise TypeError("pool must be a PagedPool")
-    return {n: getattr(pool, n) for n in ("k_pages", "v_pages", "log_beta_pages", "pos_pages", "table", "len",
-                                          "free_pages", "free_count")}
+    return (pool.k_pages, pool.v_pages, pool.log_beta_pages, pool.pos_pages, pool.table, pool.len, pool.free_pages,
+            pool.free_count)
+
+
+def _pool_bytes(pool, tensors):
+    """A packed kvb_paged_cache."""
+    return _lib.PAGED_CACHE.pack(*(0 if x is None else x.data_ptr() for x in tensors), pool.B, pool.Hkv, pool.d,
+                                 pool.max_pages, pool.num_pages)
 
 
 def kvb_paged_plan_workspace_bytes(B: int, Hkv: int) -> int:
@@ -796,16 +829,18 @@ def kvb_paged_plan(pool, cu, slot_map, workspace, *, empty_only: bool = False, s
     least kvb_paged_plan_workspace_bytes(B, Hkv) bytes. empty_only: sequences that hold slots
     already are not served."""
     tensors = _pool_tensors(pool)
-    _shape(cu, (pool.B + 1,), "cu")
-    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 2 or slot_map.shape[0] != pool.Hkv:
+    _is(cu, _I32, (pool.B + 1,), "cu")
+    if not isinstance(slot_map, torch.Tensor):
+        raise TypeError("slot_map must be a torch.Tensor")
+    if slot_map.dim() != 2 or slot_map.shape[0] != pool.Hkv:
         raise ValueError("slot_map must be [Hkv, T]")
-    for name, x in (("cu", cu), ("slot_map", slot_map)):
-        _need(x, torch.int32, name, cuda=False); _contig(x, name)
-    _need(workspace, torch.uint8, "workspace", cuda=False); _contig(workspace, "workspace")
-    dev = _one_device(dict(tensors, cu=cu, slot_map=slot_map, workspace=workspace))
-    _launch(dev, stream, lambda s: _lib.lib().kvb_paged_plan(
-        _pool(pool), _ptr(cu), int(slot_map.shape[1]), _ptr(slot_map), int(bool(empty_only)), _ptr(workspace),
-        workspace.numel(), s), "kvb_paged_plan")
+    _is(slot_map, _I32, slot_map.shape, "slot_map")
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    _is(workspace, _U8, workspace.shape, "workspace")
+    dev = _one_device(cu, slot_map, workspace, *tensors)
+    _launch(dev, stream, "kvb_paged_plan", _lib.lib().kvb_paged_plan, _pool_bytes(pool, tensors), cu.data_ptr(),
+            slot_map.shape[1], slot_map.data_ptr(), 1 if empty_only else 0, workspace.data_ptr(), workspace.numel())
 
 
 def kvb_paged_write(pool, k, v, log_beta, pos, slot_map, *, stream=None) -> None:
@@ -813,25 +848,22 @@ def kvb_paged_write(pool, k, v, log_beta, pos, slot_map, *, stream=None) -> None
     pool holds log betas) and pos [T] int32 into the pool rows that slot_map [Hkv, T] names; see
     kvb_paged_write in include/kvb.h."""
     tensors = _pool_tensors(pool)
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+    if not isinstance(k, torch.Tensor):
+        raise TypeError("k must be a torch.Tensor")
+    if k.dim() != 3:
         raise ValueError("k and v must be [T, Hkv, d]")
-    T = int(k.shape[0])
-    for name, x, shp in (("k", k, (T, pool.Hkv, pool.d)), ("v", v, (T, pool.Hkv, pool.d)),
-                         ("log_beta", log_beta, (T, pool.Hkv)), ("pos", pos, (T,)), ("slot_map", slot_map, (pool.Hkv, T))):
-        _shape(x, shp, name)
+    T, H, d = k.shape[0], pool.Hkv, pool.d
     if (log_beta is None) != (pool.log_beta_pages is None):
         raise ValueError("log_beta is needed exactly when the pool holds log betas")
-    for name, x in (("k", k), ("v", v)):
-        _need(x, torch.bfloat16, name, cuda=False)
-    for name, x in (("pos", pos), ("slot_map", slot_map)):
-        _need(x, torch.int32, name, cuda=False); _contig(x, name)
+    _is(k, _BF16, (T, H, d), "k", False)
+    _is(v, _BF16, (T, H, d), "v", False)
+    _is(pos, _I32, (T,), "pos")
+    _is(slot_map, _I32, (H, T), "slot_map")
     if log_beta is not None:
-        _need(log_beta, torch.float32, "log_beta", cuda=False)
-    ks, vs = (_packed_strides(x, T, pool.Hkv, n) for x, n in ((k, "k"), (v, "v")))
-    if ks != vs:
-        raise ValueError("k and v need equal strides")
-    ls = (0, 0) if log_beta is None else _f32_strides(log_beta, T, pool.Hkv)
-    dev = _one_device(dict(tensors, k=k, v=v, log_beta=log_beta, pos=pos, slot_map=slot_map))
-    _launch(dev, stream, lambda s: _lib.lib().kvb_paged_write(
-        _pool(pool), _ptr(k), _ptr(v), ks[0], ks[1], _ptr(log_beta), ls[0], ls[1], _ptr(pos), _ptr(slot_map), T, s),
-        "kvb_paged_write")
+        _is(log_beta, _F32, (T, H), "log_beta", False)
+    kt, kh = _kv_strides(k, v, T, H, d)
+    lt, lh = _lb_strides(log_beta, T, H)
+    dev = _one_device(k, v, log_beta, pos, slot_map, *tensors)
+    _launch(dev, stream, "kvb_paged_write", _lib.lib().kvb_paged_write, _pool_bytes(pool, tensors), k.data_ptr(),
+            v.data_ptr(), kt, kh, 0 if log_beta is None else log_beta.data_ptr(), lt, lh, pos.data_ptr(),
+            slot_map.data_ptr(), T)

@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 for (int c = 0; c < 64; c += 2) {
                     float u, v;
                     upk2(fma2(pk2(x[c], x[c + 1]), c2, n2), u, v);
-                    if (c % 8 == 6) {   // a quarter of the exponentials on the FMA pipe
+                    if ((D == 64 || CAP) && c % 8 == 6) {   // a quarter of the exponentials on the FMA pipe, as forward
                         exp2_poly2<5>(u, v);
                     } else {
                         u = ex2_approx(u);
@@ -536,6 +536,9 @@ struct DkvShape {
     static constexpr int ST = D == 128 ? 2 : 4;
     static constexpr int NT = 12 * 32;
     static constexpr int REG_SOFT = 208, REG_REST = 88;
+    // P is handed over in two halves where the products are short beside the exponentials (d 64: 681 -> 636 us
+    // at 8192 tokens, 32/8 heads); at d 128 the products bound the kernel and the extra hand-over costs (858 -> 897)
+    static constexpr bool SPLIT_P = D == 64;
     static constexpr int HALF = 128 * 128, TILE = HALF * (D / 64);
     static constexpr int K_OFF = 0;                      // K, V
     static constexpr int QO_OFF = K_OFF + 2 * TILE;      // [ST] Q, dO
@@ -547,7 +550,7 @@ struct DkvShape {
     static constexpr int DB_OFF = TOK_OFF + 64 * 4;      // [128] d log beta of the second warpgroup's columns
     static constexpr int INFO_OFF = DB_OFF + KT * 4;
     static constexpr int BAR_OFF = INFO_OFF + 2 * 8 * 4;
-    static constexpr int NBAR = 2 + 3 * ST + 6 + 4;
+    static constexpr int NBAR = 2 + 3 * ST + 7 + 4;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr size_t SMEM = 1024 + MISC_OFF + 32;
     static constexpr int TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 384, TM_COLS = 512;
@@ -573,10 +576,11 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
     uint64_t* x_full = q_empty + ST;     // extra columns, row values; rows past the document cleared
     uint64_t* s_full = x_full + ST;
     uint64_t* dp_full = s_full + 1;
-    uint64_t* p_full = s_full + 2;
-    uint64_t* ds_full = s_full + 3;
-    uint64_t* o_full = s_full + 4;       // dV, dK
-    uint64_t* db_full = s_full + 5;      // the second warpgroup's part of d log beta
+    uint64_t* p_half = s_full + 2;       // the weights of each half's first 32 columns, all of them
+    uint64_t* p_full = s_full + 3;
+    uint64_t* ds_full = s_full + 4;
+    uint64_t* o_full = s_full + 5;       // dV, dK
+    uint64_t* db_full = s_full + 6;      // the second warpgroup's part of d log beta
     uint64_t* u_full = db_full + 1;
     uint64_t* u_empty = u_full + 2;
     int* info = reinterpret_cast<int*>(smem + SH::INFO_OFF);
@@ -597,6 +601,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
         }
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
+        mbar_init(p_half, 8);
         mbar_init(p_full, 8);
         mbar_init(ds_full, 8);
         mbar_init(o_full, 1);
@@ -819,10 +824,10 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                           idesc_s, 1u);   // - delta
                 umma_commit(dp_full);
             };
-            // P^T and dS^T: a warpgroup's 64 columns as 32 words at the start of its half
-            auto grad = [&](uint32_t d, uint32_t a, uint32_t b, bool fresh) {
-                umma_rows<4>(d, a, b, idesc_o, fresh);
-                umma_rows<4>(d, a + 64, b + 64 * 128 / 16, idesc_o, false);
+            // P^T and dS^T: a warpgroup's 64 columns as 32 words at the start of its half; 32 columns of each
+            auto grad_half = [&](uint32_t d, uint32_t a, uint32_t b, bool fresh) {
+                umma_rows<2>(d, a, b, idesc_o, fresh);
+                umma_rows<2>(d, a + 64, b + 64 * 128 / 16, idesc_o, false);
             };
             auto loaded = [&](int k) {
                 return warp_wait(&q_full[k % ST], (unsigned)(k / ST) & 1u, p.wait_ns) &&
@@ -849,17 +854,26 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     const int st = step % ST, nst = (step + 1) % ST;
                     const bool more = q + 1 < n;
                     const uint32_t rows = qr_lo + st * (2 * SH::TILE >> 4);
+                    if (SH::SPLIT_P) {
+                        if (!warp_wait(p_half, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
+                        tc_fence_after();
+                        if (elect_one()) grad_half(tmem + SH::TM_DV, tmem + SH::TM_S, rows + (SH::TILE >> 4), q == 0);
+                        __syncwarp();
+                    }
+                    if (more && !loaded(step + 1)) { stop = true; break; }
                     if (!warp_wait(p_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                     tc_fence_after();
-                    if (elect_one()) grad(tmem + SH::TM_DV, tmem + SH::TM_S, rows + (SH::TILE >> 4), q == 0);
-                    __syncwarp();
-                    if (more && !loaded(step + 1)) { stop = true; break; }
-                    if (elect_one() && more) scores(nst, (b0 + q + 1) * bt >= last);
+                    if (elect_one()) {
+                        if (!SH::SPLIT_P) grad_half(tmem + SH::TM_DV, tmem + SH::TM_S, rows + (SH::TILE >> 4), q == 0);
+                        grad_half(tmem + SH::TM_DV, tmem + SH::TM_S + 16, rows + (SH::TILE >> 4) + 32 * 128 / 16, false);
+                        if (more) scores(nst, (b0 + q + 1) * bt >= last);
+                    }
                     __syncwarp();
                     if (!warp_wait(ds_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                     tc_fence_after();
                     if (elect_one()) {
-                        grad(tmem + SH::TM_DK, tmem + SH::TM_DP, rows, q == 0);
+                        grad_half(tmem + SH::TM_DK, tmem + SH::TM_DP, rows, q == 0);
+                        grad_half(tmem + SH::TM_DK, tmem + SH::TM_DP + 16, rows + 32 * 128 / 16, false);
                         umma_commit(&q_empty[st]);
                         if (more) {
                             pulls(nst);
@@ -947,7 +961,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     for (int e = 0; e < 32; e += 2) {
                         float a, b;
                         upk2(mul2(pk2(x[c0 + e], x[c0 + e + 1]), c2), a, b);
-                        if (e % 8 == 6) {   // a quarter of the exponentials on the FMA pipe
+                        if ((D == 64 || CAP) && e % 8 == 6) {   // a quarter of the exponentials on the FMA pipe, as forward
                             exp2_poly2<5>(a, b);
                         } else {
                             a = ex2_approx(a);
@@ -958,11 +972,13 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         w[e / 2] = pack_bf16(a, b);   // P and dS enter the gradients' products as bf16: 2^-9 each
                     }
                     tmem_st16(tl + SH::TM_S + t * 64 + c0 / 2, w);
+                    if (SH::SPLIT_P || c0 > 0) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(c0 == 0 ? p_half : p_full);
+                    }
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full);
                 // ---- dS
                 if (!warp_wait(dp_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();

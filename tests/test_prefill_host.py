@@ -164,3 +164,15 @@ def test_structs_match_the_header(struct, mirror):
         decl = re.sub(r"^(const\s+)?\w+\s*\**\s*", "", decl.strip())
         names += [n.strip().lstrip("*") for n in decl.split(",") if n.strip()]
     assert names == [f[0] for f in mirror._fields_]
+
+
+def test_packed_structs_have_the_mirrors_layout():
+    """The binding packs the structs as bytes: field by field the same as the ctypes mirrors."""
+    a = dict(q=1, q_stride_t=2, q_stride_h=3, k=4, v=5, kv_stride_t=6, kv_stride_h=7, log_beta=8, lb_stride_t=9, lb_stride_h=10,
+             cu=11, prefix_len=12, T=13, N=14, Hq=15, Hkv=16, d=17, scale=0.5, softcap=2.0, o=18, lse=19)
+    assert bytes(_lib.PrefillArgs(**a)) == _lib.PREFILL_ARGS.pack(*a.values())
+    g = dict(d_o=1, d_lse=2, dq=3, dk=4, dv=5, d_log_beta=6, workspace=7, workspace_bytes=8)
+    assert bytes(_lib.PrefillGrads(**g)) == _lib.PREFILL_GRADS.pack(*g.values())
+    c = [n for n, _ in _lib.PagedCacheArgs._fields_]
+    values = dict(zip(c, range(1, len(c) + 1)))
+    assert bytes(_lib.PagedCacheArgs(**values)) == _lib.PAGED_CACHE.pack(*values.values())
