@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const float C = CAP ? 1.f : p.scale * kLog2e;
         const float cap2 = CAP ? p.softcap * kLog2e : 0.f, per_cap = CAP ? p.scale / p.softcap : 0.f;
+        const float inv_cap2 = CAP ? -1.f / (cap2 * cap2) : 0.f;
         float* s_est = reinterpret_cast<float*>(smem + SH::EST_OFF);
         float* s_sum = s_est + R;
         int step = 0;
@@ -417,23 +418,18 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_read);
+                const bool past = (tile + 1) * KT <= first + 1;
                 if (CAP) {
-                    cap_tanh<64>(x, th, per_cap);
+                    cap_scores(x, per_cap, cap2);
+                    cap_scores(x + 32, per_cap, cap2);
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) x[c] = cap2 * th[c];
+                    for (int c = 0; c < 64; ++c) th[c] = x[c];
                 }
-                if (BETA && (CAP || (tile + 1) * KT > first + 1)) {
+                if (BETA && (CAP || !past)) {
                     if (!warp_wait(&x_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
                     const float4* lb = reinterpret_cast<const float4*>(smem + SH::LB_OFF + (st * KT + 64 * t) * 4);
-                    const float di = (float)(i - j0);
-#pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        const float4 b = lb[c / 4];
-                        x[c] = fmaf(fmaxf(di - c, 0.f), b.x, x[c]);
-                        x[c + 1] = fmaf(fmaxf(di - (c + 1), 0.f), b.y, x[c + 1]);
-                        x[c + 2] = fmaf(fmaxf(di - (c + 2), 0.f), b.z, x[c + 2]);
-                        x[c + 3] = fmaf(fmaxf(di - (c + 3), 0.f), b.w, x[c + 3]);
-                    }
+                    add_bias(x, lb, (float)(i - j0), past);
+                    add_bias(x + 32, lb + 8, (float)(i - j0 - 32), past);
                 }
                 if (j0 + 64 > max(first + 1, pre)) {
 #pragma unroll
@@ -467,11 +463,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                         const uint64_t ds = mul2(pk2(x[c0 + e], x[c0 + e + 1]), add2(pk2(dp[e], dp[e + 1]), e2));
                         sum = add2(sum, ds);
                         float u, v;
-                        upk2(ds, u, v);
-                        if (CAP) {
-                            u *= 1.f - th[c0 + e] * th[c0 + e];
-                            v *= 1.f - th[c0 + e + 1] * th[c0 + e + 1];
-                        }
+                        upk2(CAP ? mul2(ds, cap_slope2(th[c0 + e], th[c0 + e + 1], inv_cap2)) : ds, u, v);
                         w[e / 2] = pack_bf16(u, v);   // dS enters dS K as bf16: 2^-9 each, as dq's own rounding
                     }
                     tmem_st16(tl + SH::TM_DP + t * 64 + c0 / 2, w);
@@ -896,6 +888,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const float C = CAP ? 1.f : p.scale * kLog2e;
         const float cap2 = CAP ? p.softcap * kLog2e : 0.f, per_cap = CAP ? p.scale / p.softcap : 0.f;
+        const float inv_cap2 = CAP ? -1.f / (cap2 * cap2) : 0.f;
         const float4* tok4 = reinterpret_cast<const float4*>(smem + SH::TOK_OFF);
         float* s_db = reinterpret_cast<float*>(smem + SH::DB_OFF);
         int step = 0;
@@ -928,17 +921,28 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 if (CAP) {
                     if (!warp_wait(&x_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
                     const float4* l4 = reinterpret_cast<const float4*>(smem + SH::ROW_OFF + (st * QT + 64 * t) * 4);
-                    cap_tanh<64>(x, th, per_cap);
+                    cap_scores(x, per_cap, cap2);
+                    cap_scores(x + 32, per_cap, cap2);
+                    // + (di + c >> lg) b where all is past: by blocks of eight columns
+                    const float in_block = BETA && past ? slope_b : 0.f, per_block = in_block * (float)(8 >> lg);
+                    uint64_t by2[4];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) by2[e / 2] = pk2((float)(e >> lg) * in_block, (float)((e + 1) >> lg) * in_block);
+                    float block = di * in_block;
 #pragma unroll
                     for (int c = 0; c < 64; c += 4) {
                         const float4 l = l4[c / 4];
-                        x[c] = fmaf(cap2, th[c], -l.x);
-                        x[c + 1] = fmaf(cap2, th[c + 1], -l.y);
-                        x[c + 2] = fmaf(cap2, th[c + 2], -l.z);
-                        x[c + 3] = fmaf(cap2, th[c + 3], -l.w);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) th[c + e] = x[c + e];
+                        const uint64_t at = same2(block);
+                        const uint64_t u = add2(add2(by2[(c / 2) & 3], at), pk2(-l.x, -l.y));
+                        const uint64_t w = add2(add2(by2[(c / 2 + 1) & 3], at), pk2(-l.z, -l.w));
+                        upk2(add2(pk2(x[c], x[c + 1]), u), x[c], x[c + 1]);
+                        upk2(add2(pk2(x[c + 2], x[c + 3]), w), x[c + 2], x[c + 3]);
+                        if (c % 8 == 4) block += per_block;
                     }
                 }
-                if (BETA && (CAP || !past)) {
+                if (BETA && !past) {
 #pragma unroll
                     for (int c = 0; c < 64; c += 4) {
                         const float4 k4 = tok4[c / 4];
@@ -960,7 +964,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float a, b;
-                        upk2(mul2(pk2(x[c0 + e], x[c0 + e + 1]), c2), a, b);
+                        upk2(CAP ? pk2(x[c0 + e], x[c0 + e + 1]) : mul2(pk2(x[c0 + e], x[c0 + e + 1]), c2), a, b);
                         if ((D == 64 || CAP) && e % 8 == 6) {   // a quarter of the exponentials on the FMA pipe, as forward
                             exp2_poly2<5>(a, b);
                         } else {
@@ -994,11 +998,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         const uint64_t d = mul2(pk2(x[c0 + e], x[c0 + e + 1]), pk2(dp[e], dp[e + 1]));
                         ds[(c0 + e) / 2] = d;
                         float a, b;
-                        upk2(d, a, b);
-                        if (CAP) {
-                            a *= 1.f - th[c0 + e] * th[c0 + e];
-                            b *= 1.f - th[c0 + e + 1] * th[c0 + e + 1];
-                        }
+                        upk2(CAP ? mul2(d, cap_slope2(th[c0 + e], th[c0 + e + 1], inv_cap2)) : d, a, b);
                         w[e / 2] = pack_bf16(a, b);
                     }
                     tmem_st16(tl + SH::TM_DP + t * 64 + c0 / 2, w);

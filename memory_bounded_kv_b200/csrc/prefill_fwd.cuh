@@ -417,20 +417,11 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                         float y[32];
                         tmem_ld32(ts + c0, y);
                         tmem_ld_wait();
-                        if (CAP) cap_tanh<32>(y, y, per_cap);
-                        const float di = (float)(i - j0 - c0);
-                        const int seen = lim - j0 - c0;
+                        if (CAP) cap_scores(y, per_cap, cap2);
+                        if (biased) add_bias(y, lb + c0 / 4, (float)(i - j0 - c0), j0 + KT <= first + 1);
+                        if (masked) {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 b = biased ? lb[(c0 + c) / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
-                            const float bs[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float a = y[c + e];
-                                if (CAP) a *= cap2;
-                                if (BETA) a = fmaf(fmaxf(di - (c + e), 0.f), bs[e], a);
-                                y[c + e] = c + e < seen ? a : -INFINITY;
-                            }
+                            for (int c = 0; c < 32; ++c) y[c] = c < lim - j0 - c0 ? y[c] : -INFINITY;
                         }
                         tmem_st32(ts + c0, reinterpret_cast<const uint32_t*>(y));
                     }

@@ -186,27 +186,55 @@ __device__ __forceinline__ void store_bf16x32(uint4* dst, const float (&o)[32], 
 // tanh(y) = 1 - 2 / (1 + e^2y): off by about 2^-23 absolute
 __device__ __forceinline__ float tanh_exp(float y) { return 1.f - 2.f * rcp_approx(1.f + ex2_approx(2.f * kLog2e * y)); }
 
-// th = tanh(per_cap x): where a warp's values all lie in [-1/2, 1/2] (scores small beside the cap, the
-// common case) by y times the polynomial of degree 4 in y^2 whose largest relative error is smallest
-// (1.3e-8), which also keeps small values to fp32 accuracy; else through the exponential.
-template <int N>
-__device__ __forceinline__ void cap_tanh(const float (&x)[N], float* th, float per_cap) {
+// x = amp tanh(per_cap x), 32 values: where a warp's values all lie in [-1/2, 1/2] (scores small beside the
+// cap, the common case) by y times the polynomial of degree 4 in y^2 whose largest relative error is
+// smallest (1.3e-8), which also keeps small values to fp32 accuracy; else through the exponential.
+__device__ __forceinline__ void cap_scores(float* x, float per_cap, float amp) {
     float most = 0.f;
 #pragma unroll
-    for (int c = 0; c < N; c += 2) most = max3(most, fabsf(x[c]), fabsf(x[c + 1]));
+    for (int c = 0; c < 32; c += 2) most = max3(most, fabsf(x[c]), fabsf(x[c + 1]));
     if (__all_sync(kFull, most * per_cap <= 0.5f)) {
+        const uint64_t c4 = same2(amp * 0.017135005444288254f), c3 = same2(amp * -0.05298607423901558f),
+                       c2 = same2(amp * 0.13324779272079468f), c1 = same2(amp * -0.3333306908607483f), c0 = same2(amp);
 #pragma unroll
-        for (int c = 0; c < N; c += 2) {
+        for (int c = 0; c < 32; c += 2) {
             const uint64_t y = mul2(pk2(x[c], x[c + 1]), same2(per_cap)), u = mul2(y, y);
-            uint64_t r = fma2(same2(0.017135005444288254f), u, same2(-0.05298607423901558f));
-            r = fma2(r, u, same2(0.13324779272079468f));
-            r = fma2(r, u, same2(-0.3333306908607483f));
-            r = fma2(r, u, same2(1.f));
-            upk2(mul2(r, y), th[c], th[c + 1]);
+            const uint64_t r = fma2(fma2(fma2(fma2(c4, u, c3), u, c2), u, c1), u, c0);
+            upk2(mul2(r, y), x[c], x[c + 1]);
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < N; ++c) th[c] = tanh_exp(x[c] * per_cap);
+        for (int c = 0; c < 32; ++c) x[c] = amp * tanh_exp(x[c] * per_cap);
+    }
+}
+
+// the derivative 1 - tanh^2 of a pair of capped scores x = amp tanh(.); minus_inv = -1 / amp^2
+__device__ __forceinline__ uint64_t cap_slope2(float x, float y, float minus_inv) {
+    const uint64_t z = pk2(x, y);
+    return fma2(z, mul2(z, same2(minus_inv)), same2(1.f));
+}
+
+// x_c += max(dist - c, 0) b_c for 32 keys; without the maximum where all are past
+__device__ __forceinline__ void add_bias(float* x, const float4* b4, float dist, bool past) {
+    if (past) {
+        uint64_t d = pk2(dist, dist - 1.f);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            const float4 b = b4[c / 4];
+            upk2(fma2(d, pk2(b.x, b.y), pk2(x[c], x[c + 1])), x[c], x[c + 1]);
+            d = add2(d, same2(-2.f));
+            upk2(fma2(d, pk2(b.z, b.w), pk2(x[c + 2], x[c + 3])), x[c + 2], x[c + 3]);
+            d = add2(d, same2(-2.f));
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            const float4 b = b4[c / 4];
+            x[c] = fmaf(fmaxf(dist - c, 0.f), b.x, x[c]);
+            x[c + 1] = fmaf(fmaxf(dist - (c + 1), 0.f), b.y, x[c + 1]);
+            x[c + 2] = fmaf(fmaxf(dist - (c + 2), 0.f), b.z, x[c + 2]);
+            x[c + 3] = fmaf(fmaxf(dist - (c + 3), 0.f), b.w, x[c + 3]);
+        }
     }
 }
 
