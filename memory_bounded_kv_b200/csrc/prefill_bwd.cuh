@@ -63,9 +63,10 @@ struct DqShape {
     static constexpr int KX_OFF = QX_OFF + R * 32;
     static constexpr int LB_OFF = KX_OFF + ST * KT * 32;
     static constexpr int EST_OFF = LB_OFF + ST * KT * 4; // [128] estimates, [128] row sums of the second warpgroup
-    static constexpr int INFO_OFF = EST_OFF + 2 * R * 4;
+    static constexpr int PART_OFF = EST_OFF + 2 * R * 4; // [2][128] each warpgroup's part of delta (units of one tile)
+    static constexpr int INFO_OFF = PART_OFF + 2 * R * 4;
     static constexpr int BAR_OFF = INFO_OFF + 2 * 8 * 4;
-    static constexpr int NBAR = 4 + 3 * ST + 4 + 4;
+    static constexpr int NBAR = 4 + 3 * ST + 5 + 4;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr size_t SMEM = 1024 + MISC_OFF + 32;
     static constexpr int TM_Q = 0, TM_DO = 64, TM_S = 128, TM_DP = 256, TM_DQ = 384, TM_COLS = 512;
@@ -94,7 +95,8 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
     uint64_t* s_read = s_full + 1;
     uint64_t* dp_full = s_full + 2;
     uint64_t* ds_full = s_full + 3;
-    uint64_t* u_full = s_full + 4;
+    uint64_t* part_full = s_full + 4;
+    uint64_t* u_full = s_full + 5;
     uint64_t* u_empty = u_full + 2;
     int* info = reinterpret_cast<int*>(smem + SH::INFO_OFF);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + SH::MISC_OFF);
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
         mbar_init(s_read, 8);
         mbar_init(dp_full, 1);
         mbar_init(ds_full, 8);
+        mbar_init(part_full, 8);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&u_full[t], 1);
             mbar_init(&u_empty[t], 10);   // products, bias, 8 softmax warps
@@ -342,6 +345,8 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
         const float inv_cap2 = CAP ? -1.f / (cap2 * cap2) : 0.f;
         float* s_est = reinterpret_cast<float*>(smem + SH::EST_OFF);
         float* s_sum = s_est + R;
+        float* s_part = reinterpret_cast<float*>(smem + SH::PART_OFF);
+        unsigned singles = 0;   // parity of the units of one tile
         int step = 0;
         bool stop = false;
         int s = -1, len = 0, i0 = 0, g = 0, pre = 0, n = 0;
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
 #pragma unroll
                     for (int c = 0; c < 64; ++c) x[c] = c < lim - j0 ? x[c] : -INFINITY;
                 }
-                const uint64_t c2 = pk2(C, C), n2 = pk2(-lse2, -lse2), e2 = pk2(-est, -est);
+                const uint64_t c2 = same2(C), n2 = same2(-lse2);
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
                     float u, v;
@@ -452,6 +457,30 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 uint64_t sum = 0ull;
                 if (!warp_wait(dp_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
+                if (n == 1) {
+                    // all keys of these rows are here: delta itself before dS. Rows of few keys can have p near 1,
+                    // where dP - delta cancels and the estimate's error shows in dq (a document of one token has
+                    // dq = 0; two tokens: 0.0029 -> 0.0011 of dq besides its rounding)
+                    uint64_t part = 0ull;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 64; c0 += 32) {
+                        float dp[32];
+                        tmem_ld32(tl + SH::TM_DP + t * 64 + c0, dp);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            part = fma2(c0 ? pk2(x[32 + e], x[33 + e]) : pk2(x[e], x[e + 1]), pk2(dp[e], dp[e + 1]), part);
+                    }
+                    float p0, p1;
+                    upk2(part, p0, p1);
+                    s_part[t * R + r] = p0 + p1;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(part_full);
+                    if (!warp_wait(part_full, singles, p.wait_ns)) { stop = true; break; }
+                    singles ^= 1u;
+                    est = s_part[r] + s_part[R + r] - dlse;
+                }
+                const uint64_t e2 = same2(-est);
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
                     float dp[32];
