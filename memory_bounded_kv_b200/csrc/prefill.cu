@@ -170,7 +170,10 @@ kvb_status kvb_paged_plan(const kvb_paged_cache* c, const int32_t* cu, int32_t T
     kvb::PagedPlanParams p{pc, cu, slot_map, c->B, T, empty_only, static_cast<int4*>(workspace)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (launch_pdl(kvb::paged_plan_kernel<1024>, dim3(1), dim3(1024), 0, st, p) != KVB_OK) return KVB_ECUDA;
-    return launch_pdl(kvb::paged_slots_kernel<256>, dim3(c->B * c->Hkv), dim3(256), 0, st, p);
+    // a block for every 1024 tokens of a row's share (256 tokens: 16.7 us instead of 13 for 131072 tokens in 256 rows)
+    const long long share = ((long long)T / c->B + 1023) / 1024;
+    const unsigned parts = (unsigned)std::min<long long>(std::max<long long>(share, 1), 64);
+    return launch_pdl(kvb::paged_slots_kernel<256>, dim3(c->B * c->Hkv, parts), dim3(256), 0, st, p);
 }
 
 kvb_status kvb_paged_write(const kvb_paged_cache* c, const uint16_t* k, const uint16_t* v, int64_t kv_stride_t,
@@ -182,12 +185,15 @@ kvb_status kvb_paged_write(const kvb_paged_cache* c, const uint16_t* k, const ui
     if (T == 0) return KVB_OK;
     if (!k || !v || !pos || !slot_map || !aligned16(k) || !aligned16(v) || !aligned4(pos) || !aligned4(slot_map)) return KVB_EINVAL;
     if ((c->log_beta_pages != nullptr) != (log_beta != nullptr) || !aligned4(log_beta)) return KVB_EINVAL;
+    if (c->Hkv > 65535) return KVB_EINVAL;
     if (kv_stride_t < 0 || kv_stride_h < 0 || kv_stride_t % 8 || kv_stride_h % 8 || lb_stride_t < 0 || lb_stride_h < 0)
         return KVB_EINVAL;
     kvb::PagedWriteParams p{pc, k, v, log_beta, pos, slot_map, kv_stride_t, kv_stride_h, lb_stride_t, lb_stride_h, T};
-    const long long n = (long long)T * c->Hkv * (c->d / 8);
-    const unsigned grid = (unsigned)std::min<long long>((n + 255) / 256, 148 * 8);
-    return launch_pdl(kvb::paged_write_kernel, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), p);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int groups = 256 / (c->d / 8);
+    const long long blocks = ((long long)T + groups - 1) / groups * c->Hkv;
+    if (blocks > 0x7fffffffLL) return KVB_EINVAL;
+    return launch_pdl(kvb::paged_write_kernel, dim3((unsigned)blocks), dim3(256), 0, st, p);
 }
 
 }  // extern "C"

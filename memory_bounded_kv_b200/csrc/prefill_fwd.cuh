@@ -151,9 +151,8 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REG_REST));
     if (warp == 9) {
         // ======================= units and loads =======================
-        const bool ok = prefill_docs_ok(p.cu, p.N, p.T);
         const PrefillWalk walk(p, sh);
-        const long long units = ok ? walk.units : 0;
+        const long long units = walk.units;
         int step = 0, uc = 0;
         bool stop = false;
         for (long long r = 0; !stop; ++r, ++uc) {

@@ -28,15 +28,6 @@ struct PrefillParams {
     float* dlb;               // [T, Hkv] or null
 };
 
-// Whether cu is in order and inside [0, T]; the same for the whole warp. Records KVB_DERR_RANGE if not.
-__device__ __forceinline__ bool prefill_docs_ok(const int* cu, int N, int T) {
-    bool bad = false;
-    for (int n = threadIdx.x & 31; n < N; n += 32) bad |= cu[n] < 0 || cu[n + 1] < cu[n] || cu[n + 1] > T;
-    bad = __any_sync(kFull, bad);
-    if (bad && (threadIdx.x & 31) == 0) raise_error(KVB_DERR_RANGE);
-    return !bad;
-}
-
 // A unit: block `blk` of 2^sh tokens of a document (rows s .. s + len) and a kv head.
 struct PrefillUnit {
     int s, len, blk, g, pre;
@@ -44,24 +35,38 @@ struct PrefillUnit {
 
 // The units in an order of falling work, found from cu alone (the host does not know the lengths):
 // level b holds block b of every document that has one, for every kv head, and later blocks see more
-// keys. A whole warp walks it; the blocks of document `lane` stay in a register.
+// keys. A whole warp walks it; document `lane`'s bounds stay in registers. With cu out of order or
+// outside [0, T] there are no units (KVB_DERR_RANGE).
 struct PrefillWalk {
     const int* cu;
     const int* prefix;
-    int N, Hkv, sh, lane, t0, levels;
+    int N, Hkv, sh, lane, s0, e0, levels;
     long long units;
 
-    __device__ __forceinline__ int blocks(int n) const { return n < N ? (cu[n + 1] - cu[n] + (1 << sh) - 1) >> sh : 0; }
+    __device__ __forceinline__ int blocks_of(int s, int e) const { return (e - s + (1 << sh) - 1) >> sh; }
+    __device__ __forceinline__ int blocks(int n) const { return n < N ? blocks_of(cu[n], cu[n + 1]) : 0; }
     // blocks of level >= b, all documents
     __device__ __forceinline__ int count(int b) const {
-        int c = max(t0 - b, 0);
+        int c = max(blocks_of(s0, e0) - b, 0);
         for (int n = lane + 32; n < N; n += 32) c += max(blocks(n) - b, 0);
         return __reduce_add_sync(kFull, c);
     }
     __device__ __forceinline__ PrefillWalk(const PrefillParams& p, int sh_)
         : cu(p.cu), prefix(p.prefix), N(p.N), Hkv(p.Hkv), sh(sh_), lane(threadIdx.x & 31) {
-        levels = t0 = blocks(lane);
-        for (int n = lane + 32; n < N; n += 32) levels = max(levels, blocks(n));
+        s0 = lane < N ? cu[lane] : 0;
+        e0 = lane < N ? cu[lane + 1] : 0;
+        bool bad = s0 < 0 || e0 < s0 || e0 > p.T;
+        levels = blocks_of(s0, e0);
+        for (int n = lane + 32; n < N; n += 32) {
+            const int s = cu[n], e = cu[n + 1];
+            bad |= s < 0 || e < s || e > p.T;
+            levels = max(levels, blocks_of(s, e));
+        }
+        if (__any_sync(kFull, bad)) {
+            if (lane == 0) raise_error(KVB_DERR_RANGE);
+            units = 0;
+            return;
+        }
         levels = __reduce_max_sync(kFull, levels);
         units = (long long)count(0) * Hkv;
     }
@@ -81,7 +86,7 @@ struct PrefillWalk {
         const long long at = u - (long long)above * Hkv;
         int rank = (int)(at / Hkv), doc = 0;
         for (int n0 = 0; n0 < N; n0 += 32) {
-            const bool has = (n0 == 0 ? t0 : blocks(n0 + lane)) > lo;
+            const bool has = (n0 == 0 ? blocks_of(s0, e0) : blocks(n0 + lane)) > lo;
             const unsigned m = __ballot_sync(kFull, has);
             const int c = __popc(m);
             if (rank < c) {
@@ -92,8 +97,15 @@ struct PrefillWalk {
             rank -= c;
         }
         PrefillUnit x;
-        x.s = cu[doc];
-        x.len = cu[doc + 1] - x.s;
+        int e;
+        if (doc < 32) {
+            x.s = __shfl_sync(kFull, s0, doc);
+            e = __shfl_sync(kFull, e0, doc);
+        } else {
+            x.s = cu[doc];
+            e = cu[doc + 1];
+        }
+        x.len = e - x.s;
         x.blk = lo;
         x.g = (int)(at % Hkv);
         x.pre = prefix == nullptr ? 0 : min(max(prefix[doc], 0), x.len);
@@ -175,12 +187,23 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-// 32 values times f, as bf16, to 64 bytes
-__device__ __forceinline__ void store_bf16x32(uint4* dst, const float (&o)[32], float f) {
+// 32 values times f, as bf16, to 64 bytes of a row; a thread writes its own row, so a store touches 32
+// lines: in 32 bytes each (whole sectors, half the stores) where the address allows
+__device__ __forceinline__ void store_bf16x32(void* dst, const float (&o)[32], float f) {
+    uint32_t w[16];
 #pragma unroll
-    for (int c = 0; c < 32; c += 8)
-        dst[c / 8] = make_uint4(pack_bf16(o[c] * f, o[c + 1] * f), pack_bf16(o[c + 2] * f, o[c + 3] * f),
-                                pack_bf16(o[c + 4] * f, o[c + 5] * f), pack_bf16(o[c + 6] * f, o[c + 7] * f));
+    for (int c = 0; c < 16; ++c) w[c] = pack_bf16(o[2 * c] * f, o[2 * c + 1] * f);
+    if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+#pragma unroll
+        for (int c = 0; c < 16; c += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<uint32_t*>(dst) + c),
+                         "r"(w[c]), "r"(w[c + 1]), "r"(w[c + 2]), "r"(w[c + 3]), "r"(w[c + 4]), "r"(w[c + 5]), "r"(w[c + 6]),
+                         "r"(w[c + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) static_cast<uint4*>(dst)[c / 4] = make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+    }
 }
 
 // tanh(y) = 1 - 2 / (1 + e^2y): off by about 2^-23 absolute
