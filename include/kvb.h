@@ -422,8 +422,9 @@ kvb_status kvb_paged_compact_blocks(const kvb_paged_cache* cache, const int32_t*
  *   dk, dv [T, Hkv, d] bf16, d_log_beta [T, Hkv] f32 (given exactly when
  *   log_beta is): contiguous
  *   workspace: kvb_prefill_attn_bwd_workspace_bytes(T, Hq) bytes, 16-byte
- *   aligned; no content is read before it is written. Calls that may run at
- *   the same time need workspaces of their own.
+ *   aligned (4 T Hq bytes for delta, 42 MB for the sums of key blocks that
+ *   several CTAs share); no content is read before it is written. Calls that
+ *   may run at the same time need workspaces of their own.
  * Rows of no document are neither read into a result nor written. A document
  * may be empty. cu out of order or outside [0, T] sets KVB_DERR_RANGE and
  * nothing is written.

@@ -22,6 +22,8 @@
 //   By keys there is no room for that (dK, dV, S and dP fill the tensor memory). S and dP alternate:
 // P done -> dV += P^T dO and the next S, while the warpgroups turn dP into dS; dS done -> dK += dS^T Q
 // and the next dP, while they turn the next S into P.
+// Its key blocks are cut into pieces of equal length for the CTAs (StepLine), and prefill_dkv_sum_kernel
+// adds up the few that a cut goes through.
 //   The two warpgroups share a tile: each takes 64 of its 128 columns, a thread per row.
 // The bias rides the S product as in prefill_fwd_kernel; by keys, - lse and - delta ride S and dP too.
 #pragma once
@@ -668,35 +670,58 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REG_REST));
         if (warp == 9) {
             // ======================= units and loads =======================
+            const StepLine line(p);
+            const bool cut = line.cut(gridDim.x);
+            const long long piece = line.piece(gridDim.x), x1 = min((blockIdx.x + 1) * piece, line.steps);
             const PrefillWalk walk(p, 7);
-            const long long units = walk.units;
             int step = 0, uc = 0;
             bool stop = false;
-            for (long long r = 0; !stop; ++r, ++uc) {
-                const long long u = PrefillWalk::nth(r, blockIdx.x, gridDim.x);
-                const bool end = r * gridDim.x >= units;
-                if (!end && u >= units) { --uc; continue; }
-                PrefillUnit x{};
-                int j0 = 0, b0 = 0, b1 = 0;
-                if (!end) {
-                    x = walk.unit(u);
-                    // the first keys meet the most queries: the heaviest level is block 0
-                    j0 = ((x.len + KT - 1) / KT - 1 - x.blk) * KT;
-                    b0 = j0 < x.pre ? 0 : j0 / bt;
-                    b1 = (x.len + bt - 1) / bt;
+            long long x = blockIdx.x * piece, round = 0;
+            for (;; ++uc) {
+                bool end;
+                int s = 0, len = 0, g = 0, pre = 0, j0 = 0, b0 = 0, b1 = 0, part = 0;
+                if (cut) {
+                    end = x >= x1;
+                    if (!end) {
+                        const StepLine::At u = line.find(x);
+                        const long long till = min(u.end, x1);
+                        s = u.d.s, len = u.d.len, pre = u.d.pre, g = u.g;
+                        j0 = u.kb * KT;
+                        b0 = u.b0 + (int)(x - u.begin);
+                        b1 = u.b0 + (int)(till - u.begin);
+                        // a whole key block (0), one that began in an earlier piece (1), one that goes on in the next (2)
+                        part = x > u.begin ? 1 : (till < u.end ? 2 : 0);
+                        x = till;
+                    }
+                } else {
+                    long long u = PrefillWalk::nth(round, blockIdx.x, gridDim.x);
+                    end = round * gridDim.x >= walk.units;
+                    if (!end && u >= walk.units) {
+                        end = true;   // a last round without this CTA
+                    }
+                    if (!end) {
+                        const PrefillUnit w = walk.unit(u);
+                        s = w.s, len = w.len, pre = w.pre, g = w.g;
+                        // the first keys meet the most queries: the heaviest level is block 0
+                        j0 = ((len + KT - 1) / KT - 1 - w.blk) * KT;
+                        b0 = j0 < pre ? 0 : j0 / bt;
+                        b1 = (len + bt - 1) / bt;
+                        ++round;
+                    }
                 }
                 const int ub = uc & 1;
                 if (uc >= 2 && !warp_wait(&u_empty[ub], (unsigned)((uc >> 1) - 1) & 1u, p.wait_ns)) { stop = true; break; }
                 if (__any_sync(kFull, *s_abort != 0)) break;
                 if (lane == 0) {
                     int* m = info + ub * 8;
-                    m[0] = end ? -1 : x.s;
-                    m[1] = x.len;
+                    m[0] = end ? -1 : s;
+                    m[1] = len;
                     m[2] = j0;
-                    m[3] = x.g;
-                    m[4] = x.pre;
+                    m[3] = g;
+                    m[4] = pre;
                     m[5] = b0;
                     m[6] = b1;
+                    m[7] = part;
                     mbar_arrive(&u_full[ub]);
                 }
                 __syncwarp();
@@ -706,8 +731,8 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     mbar_arrive_expect_tx(k_full, (unsigned)(2 * SH::TILE));
                     for (int h = 0; h < D / 64; ++h) {
                         unsigned char* at = smem + SH::K_OFF + h * SH::HALF;
-                        tma_load_3d(at, &tmK, 64 * h, x.g, x.s + j0, k_full);
-                        tma_load_3d(at + SH::TILE, &tmV, 64 * h, x.g, x.s + j0, k_full);
+                        tma_load_3d(at, &tmK, 64 * h, g, s + j0, k_full);
+                        tma_load_3d(at + SH::TILE, &tmV, 64 * h, g, s + j0, k_full);
                     }
                     s_steps[1] = uc + 1;
                 }
@@ -718,13 +743,14 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         mbar_arrive_expect_tx(&q_full[st], (unsigned)(2 * SH::TILE));
                         for (int h = 0; h < D / 64; ++h) {
                             unsigned char* at = smem + SH::QO_OFF + st * 2 * SH::TILE + h * SH::HALF;
-                            tma_load_3d(at, &tmQ, 64 * h, x.g << lg, x.s + b * bt, &q_full[st]);
-                            tma_load_3d(at + SH::TILE, &tmO, 64 * h, x.g << lg, x.s + b * bt, &q_full[st]);
+                            tma_load_3d(at, &tmQ, 64 * h, g << lg, s + b * bt, &q_full[st]);
+                            tma_load_3d(at + SH::TILE, &tmO, 64 * h, g << lg, s + b * bt, &q_full[st]);
                         }
                         s_steps[0] = step + 1;
                     }
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
+                if (stop) break;
             }
             if (stop && lane == 0) fail();
         } else if (warp >= 10) {
@@ -924,7 +950,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             const int ub = uc & 1;
             if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
             const int* m = info + ub * 8;
-            const int s = m[0], len = m[1], j0 = m[2], g = m[3], pre = m[4], b0 = m[5], b1 = m[6];
+            const int s = m[0], len = m[1], j0 = m[2], g = m[3], pre = m[4], b0 = m[5], b1 = m[6], part = m[7];
             __syncwarp();
             if (lane == 0) mbar_arrive(&u_empty[ub]);
             if (s < 0) break;
@@ -1078,12 +1104,18 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             if (!warp_wait(o_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
             tc_fence_after();
             uint4* dst = reinterpret_cast<uint4*>((t ? p.dk : p.dv) + ((size_t)(s + j) * p.Hkv + g) * D);
+            float* sums = p.parts + ((size_t)blockIdx.x * 2 + (part - 1)) * kPartFloats;   // where part > 0
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 float o[32];
                 tmem_ld32(tl + (t ? SH::TM_DK : SH::TM_DV) + c0, o);
                 tmem_ld_wait();
-                if (j < len) store_bf16x32(dst + c0 / 8, o, t ? p.scale : 1.f);
+                if (part) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) sums[(t * 128 + c0 + c) * 128 + r] = o[c];
+                } else if (j < len) {
+                    store_bf16x32(dst + c0 / 8, o, t ? p.scale : 1.f);
+                }
             }
             tc_fence_before();   // the next unit's products follow this thread's next P
             if (BETA) {
@@ -1094,7 +1126,11 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     if (lane == 0) mbar_arrive(db_full);
                 } else {
                     if (!warp_wait(db_full, (unsigned)uc & 1u, p.wait_ns)) { stop = true; break; }
-                    if (j < len) p.dlb[(size_t)(s + j) * p.Hkv + g] = db + s_db[r];
+                    if (part) {
+                        sums[2 * 128 * 128 + r] = db + s_db[r];
+                    } else if (j < len) {
+                        p.dlb[(size_t)(s + j) * p.Hkv + g] = db + s_db[r];
+                    }
                 }
             }
         }
@@ -1119,6 +1155,44 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
     if (warp == 8) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SH::TM_COLS) : "memory");
+    }
+}
+
+// The key blocks that a cut goes through: the sums of their pieces, in order. blockIdx.x names the piece that
+// holds a key block's first step and not its last; a thread sums one key's 2 D / 16 columns (the parts are
+// [column][key], so that a warp's accesses are whole lines).
+template <int D, bool BETA>
+__global__ void __launch_bounds__(256) prefill_dkv_sum_kernel(const __grid_constant__ PrefillParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const StepLine line(p);
+    const long long piece = line.piece(p.pieces), x0 = blockIdx.x * piece, x1 = x0 + piece;
+    if (!line.cut(p.pieces) || x1 >= line.steps) return;
+    const StepLine::At u = line.find(x1 - 1);
+    if (u.end == x1 || u.begin < x0) return;
+    const int till = (int)((u.end - 1) / piece);   // the last piece with a part of it
+    const int r = threadIdx.x & 127, j = u.kb * 128 + r;
+    constexpr int W = 2 * D / 16;
+    const int col = (blockIdx.y * 2 + (threadIdx.x >> 7)) * W;   // of dV's D columns, then dK's
+    const int at = (col < D ? col : 128 + col - D) * 128 + r;
+    float sum[W];
+#pragma unroll
+    for (int c = 0; c < W; ++c) sum[c] = p.parts[((size_t)blockIdx.x * 2 + 1) * kPartFloats + at + c * 128];
+    for (int q = blockIdx.x + 1; q <= till; ++q)
+#pragma unroll
+        for (int c = 0; c < W; ++c) sum[c] += p.parts[(size_t)q * 2 * kPartFloats + at + c * 128];
+    if (j >= u.d.len) return;
+    const size_t row = (size_t)(u.d.s + j) * p.Hkv + u.g;
+    const float f = col < D ? 1.f : p.scale;
+    uint4* dst = reinterpret_cast<uint4*>((col < D ? p.dv : p.dk) + row * D + (col < D ? col : col - D));
+#pragma unroll
+    for (int c = 0; c < W; c += 8)
+        dst[c / 8] = make_uint4(pack_bf16(sum[c] * f, sum[c + 1] * f), pack_bf16(sum[c + 2] * f, sum[c + 3] * f),
+                                pack_bf16(sum[c + 4] * f, sum[c + 5] * f), pack_bf16(sum[c + 6] * f, sum[c + 7] * f));
+    if (BETA && col == 0) {
+        float b = p.parts[((size_t)blockIdx.x * 2 + 1) * kPartFloats + 2 * 128 * 128 + r];
+        for (int q = blockIdx.x + 1; q <= till; ++q) b += p.parts[(size_t)q * 2 * kPartFloats + 2 * 128 * 128 + r];
+        p.dlb[row] = b;
     }
 }
 

@@ -26,7 +26,12 @@ struct PrefillParams {
     uint16_t* dk;             // [T, Hkv, d]
     uint16_t* dv;             // [T, Hkv, d]
     float* dlb;               // [T, Hkv] or null
+    float* parts;             // [pieces][2] sums of key blocks that a cut goes through (kPartFloats each)
+    int pieces;
 };
+
+constexpr int kMaxPieces = 160;                          // CTAs of the kernel by keys, at most
+constexpr int kPartFloats = 2 * 128 * 128 + 128;         // dV^T, dK^T [d][128 keys], d log beta [128 keys]
 
 // A unit: block `blk` of 2^sh tokens of a document (rows s .. s + len) and a kv head.
 struct PrefillUnit {
@@ -115,6 +120,115 @@ struct PrefillWalk {
     // heaviest unit gets the next round's lightest
     __device__ __forceinline__ static long long nth(long long r, int c, int grid) {
         return r * grid + ((r & 1) ? grid - 1 - c : c);
+    }
+};
+
+// The work of the kernel by keys as one line of steps (128 query rows against 128 keys), in the order
+// (document, kv head, key block, query block), to be cut into equal pieces: the first keys of a long
+// document meet all its queries, and where there are few key blocks most CTAs would wait for those. A key
+// block that a cut goes through is summed from its pieces afterwards, in order.
+struct StepLine {
+    const int* cu;
+    const int* prefix;
+    int N, Hkv, lg, lane;
+    long long steps;   // 0 with cu out of order or outside [0, T] (KVB_DERR_RANGE)
+    int longest;       // steps of the heaviest key block
+
+    struct Doc {
+        int s, len, pre, nq, nk, np;   // query blocks, key blocks, key blocks that begin inside the prefix
+        // steps of the key blocks before kb, one kv head: the queries of block kb begin at kb 2^lg, or at 0
+        __device__ __forceinline__ long long before(int kb, int lg) const {
+            const long long k = kb, f = min(kb, np);
+            return k * nq - (((k * (k - 1) - f * (f - 1)) / 2) << lg);
+        }
+    };
+    __device__ __forceinline__ Doc doc(int n) const {
+        Doc d{};
+        if (n < N) {
+            d.s = cu[n];
+            d.len = cu[n + 1] - d.s;
+            d.pre = prefix == nullptr ? 0 : min(max(prefix[n], 0), d.len);
+            d.nq = (d.len + (128 >> lg) - 1) >> (7 - lg);
+            d.nk = (d.len + 127) >> 7;
+            d.np = (d.pre + 127) >> 7;
+        }
+        return d;
+    }
+    __device__ __forceinline__ StepLine(const PrefillParams& p)
+        : cu(p.cu), prefix(p.prefix), N(p.N), Hkv(p.Hkv), lane(threadIdx.x & 31), steps(0), longest(0) {
+        lg = 31 - __clz(p.G);
+        bool bad = false;
+        for (int n = lane; n < N; n += 32) bad |= cu[n] < 0 || cu[n + 1] < cu[n] || cu[n + 1] > p.T;
+        if (__any_sync(kFull, bad)) {
+            if (lane == 0) raise_error(KVB_DERR_RANGE);
+            return;
+        }
+        for (int n = lane; n < N; n += 32) {
+            const Doc d = doc(n);
+            steps += d.before(d.nk, lg);
+            longest = max(longest, d.nq);
+        }
+        longest = __reduce_max_sync(kFull, longest);
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) steps += __shfl_xor_sync(kFull, steps, m);
+        steps *= Hkv;
+    }
+    __device__ __forceinline__ long long piece(int pieces) const { return (steps + pieces - 1) / pieces; }
+    // Whether to cut: where one key block weighs as much as three quarters of a CTA's share. Below that whole
+    // key blocks, heaviest first, balance as well, and CTAs that walk the same queries together read them from
+    // L2 (8192 tokens, 32/8 heads, d 128: 895 us whole, 972 and the sums cut; 5003 ragged tokens, 16/4 heads,
+    // with a cap: all three kernels 461 us whole, 384 cut).
+    __device__ __forceinline__ bool cut(int pieces) const { return 4LL * longest > 3 * piece(pieces); }
+
+    struct At {
+        Doc d;
+        int g, kb, b0;            // kv head, key block, its first query block
+        long long begin, end;     // the steps of this (document, head, key block)
+    };
+    // the key block that step x of [0, steps) belongs to
+    __device__ __forceinline__ At find(long long x) const {
+        At a{};
+        long long base = 0;
+        for (int n0 = 0; n0 < N; n0 += 32) {
+            Doc d = doc(n0 + lane);
+            const long long own = d.before(d.nk, lg) * Hkv;
+            long long upto = own;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const long long y = __shfl_up_sync(kFull, upto, m);
+                if (lane >= m) upto += y;
+            }
+            const unsigned hit = __ballot_sync(kFull, base + upto > x);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                base += __shfl_sync(kFull, upto - own, l);
+                a.d.s = __shfl_sync(kFull, d.s, l);
+                a.d.len = __shfl_sync(kFull, d.len, l);
+                a.d.pre = __shfl_sync(kFull, d.pre, l);
+                a.d.nq = __shfl_sync(kFull, d.nq, l);
+                a.d.nk = __shfl_sync(kFull, d.nk, l);
+                a.d.np = __shfl_sync(kFull, d.np, l);
+                break;
+            }
+            base += __shfl_sync(kFull, upto, 31);
+        }
+        const long long per_head = a.d.before(a.d.nk, lg);
+        a.g = (int)((x - base) / per_head);
+        base += a.g * per_head;
+        int lo = 0, hi = a.d.nk;   // before(lo) <= x - base < before(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.d.before(mid, lg) <= x - base) {
+                lo = mid;
+            } else {
+                hi = mid;
+            }
+        }
+        a.kb = lo;
+        a.b0 = lo < a.d.np ? 0 : lo << lg;
+        a.begin = base + a.d.before(lo, lg);
+        a.end = base + a.d.before(lo + 1, lg);
+        return a;
     }
 };
 

@@ -115,7 +115,7 @@ def test_library_refuses(bad):
 
 
 @pytest.mark.parametrize("bad", [dict(d_o=None), dict(dq=F + 8), dict(dk=None), dict(dv=None), dict(d_log_beta=None),
-                                 dict(workspace=None), dict(workspace=F + 4), dict(workspace_bytes=T * Hq * 4 - 1)])
+                                 dict(workspace=None), dict(workspace=F + 4), dict(workspace_bytes=_lib.lib().kvb_prefill_attn_bwd_workspace_bytes(T, Hq) - 1)])
 def test_library_refuses_gradient_arguments(bad):
     g = dict(d_o=F, d_lse=None, dq=F, dk=F, dv=F, d_log_beta=F, workspace=F, workspace_bytes=1 << 30)
     L = _lib.lib()
