@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
             const int n = max(n0, n1), nt = t ? n1 : n0;
             const int i = first + (r >> lg);
             const int lim = min(max(i + 1, pre), len);
+            const int lo = __shfl_sync(kFull, lim, 0), hi = __shfl_sync(kFull, lim, 31);   // the warp's fewest and most
             step += n - nt;
             if (nt == 0) continue;
             float m_ref = -INFINITY, l_sum = 0.f;
@@ -414,13 +415,18 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
 #pragma unroll 1
                     for (int c0 = 0; c0 < KT; c0 += 32) {
                         float y[32];
-                        tmem_ld32(ts + c0, y);
-                        tmem_ld_wait();
-                        if (CAP) cap_scores(y, per_cap, cap2);
-                        if (biased) add_bias(y, lb + c0 / 4, (float)(i - j0 - c0), j0 + KT <= first + 1);
-                        if (masked) {
+                        if (masked && c0 >= hi - j0) {
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) y[c] = c < lim - j0 - c0 ? y[c] : -INFINITY;
+                            for (int c = 0; c < 32; ++c) y[c] = -INFINITY;
+                        } else {
+                            tmem_ld32(ts + c0, y);
+                            tmem_ld_wait();
+                            if (CAP) cap_scores(y, per_cap, cap2);
+                            if (biased) add_bias(y, lb + c0 / 4, (float)(i - j0 - c0), j0 + KT <= first + 1);
+                            if (masked && c0 + 32 > lo - j0) {
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) y[c] = c < lim - j0 - c0 ? y[c] : -INFINITY;
+                            }
                         }
                         tmem_st32(ts + c0, reinterpret_cast<const uint32_t*>(y));
                     }
