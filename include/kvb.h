@@ -438,7 +438,7 @@ kvb_status kvb_paged_compact_blocks(const kvb_paged_cache* cache, const int32_t*
  * the strides of q, k, v multiples of 8, at least d; scale 0 (for 1/sqrt(d))
  * or in [2^-20, 2^20]; softcap 0 or in [2^-20, 2^20].
  * ---------------------------------------------------------------------- */
-#define KVB_PREFILL_MAX_DOCS 65536
+#define KVB_PREFILL_MAX_DOCS 8192
 #define KVB_PREFILL_MAX_TOKENS (1 << 24)
 #define KVB_PREFILL_MIN_SCALE (1.0f / (1 << 20))
 
@@ -493,6 +493,8 @@ kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* args, const kvb_prefill_
  * KVB_DERR_PAGES is set. A sequence whose tokens do not fit its table, whose
  * len is out of range or, with empty_only != 0, that holds slots already while
  * it has new tokens, is not served either (KVB_DERR_LEN), and wants no pages.
+ * A page outside the pool met on the way gives its tokens slot -1 and sets
+ * KVB_DERR_RANGE.
  * slot_map entries of tokens outside all sequences are left as they were. cu
  * out of order or outside [0, T] sets KVB_DERR_RANGE: slot_map is set to -1
  * throughout and the cache is left as it was.

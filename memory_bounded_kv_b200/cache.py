@@ -175,6 +175,16 @@ class PagedKVCache:
         follow, each of which replaces a slot of a sequence that holds M or more. kvb_get_error
         tells of sequences that were not served (their o is written all the same)."""
         from . import kvb_paged_plan, kvb_paged_plan_workspace_bytes, kvb_paged_write, kvb_prefill_attn
+        # what the write below checks, before anything changes the cache
+        T = int(q.shape[0])
+        if tuple(q.shape[1:]) != (self.Hq, self.d) or tuple(k.shape) != (T, self.Hkv, self.d):
+            raise ValueError("q must be [T, Hq, d] and k, v [T, Hkv, d] of the cache's heads and d")
+        if tuple(cu.shape) != (self.B + 1,):
+            raise ValueError("cu must be [B + 1]")
+        if tuple(pos.shape) != (T,) or pos.dtype != torch.int32 or not pos.is_contiguous():
+            raise ValueError("pos must be [T] int32, contiguous")
+        if (self.pool.log_beta_pages is not None) and log_beta is None:
+            raise ValueError("log_beta is needed: the cache holds log betas")
         if stream is None:
             stream = torch.cuda.current_stream(self.pool.len.device)
         elif not isinstance(stream, torch.cuda.Stream):

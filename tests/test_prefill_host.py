@@ -99,7 +99,7 @@ def c_args(**kw):
     return _lib.PrefillArgs(**a)
 
 
-BAD = [dict(d=96), dict(Hq=6), dict(Hq=32), dict(Hkv=0), dict(T=-1), dict(T=(1 << 24) + 1), dict(N=-1), dict(N=65537),
+BAD = [dict(d=96), dict(Hq=6), dict(Hq=32), dict(Hkv=0), dict(T=-1), dict(T=(1 << 24) + 1), dict(N=-1), dict(N=8193),
        dict(q=None), dict(k=F + 2), dict(v=None), dict(cu=None), dict(o=F + 4), dict(log_beta=F + 2),
        dict(q_stride_t=Hq * d + 4), dict(q_stride_h=0), dict(kv_stride_t=-Hkv * d), dict(kv_stride_h=d - 8),
        dict(lb_stride_t=-1), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=2.0 ** -21), dict(scale=float("inf")),
@@ -176,3 +176,19 @@ def test_packed_structs_have_the_mirrors_layout():
     c = [n for n, _ in _lib.PagedCacheArgs._fields_]
     values = dict(zip(c, range(1, len(c) + 1)))
     assert bytes(_lib.PagedCacheArgs(**values)) == _lib.PAGED_CACHE.pack(*values.values())
+
+
+def test_cache_prefill_refuses_before_it_changes_anything(monkeypatch):
+    from memory_bounded_kv_b200 import cache as cache_mod
+    monkeypatch.setattr(kvb, "kvb_paged_reset", lambda pool, stream=None: None)
+    c = cache_mod.PagedKVCache(N, Hq, Hkv, d, max_pages=2, num_pages=8, M=64, device="cpu")
+    called = []
+    for f in ("kvb_prefill_attn", "kvb_paged_plan", "kvb_paged_write"):
+        monkeypatch.setattr(kvb, f, lambda *a, _f=f, **k: called.append(_f))
+    a = args()
+    good = dict(q=a["q"], k=a["k"], v=a["v"], log_beta=a["log_beta"], cu=a["cu"], pos=torch.zeros(T, dtype=torch.int32), o=a["o"])
+    for bad in (dict(log_beta=None), dict(pos=torch.zeros(T)), dict(pos=torch.zeros(T - 1, dtype=torch.int32)),
+                dict(k=a["k"][:, :1]), dict(cu=a["cu"][:-1]), dict(q=a["k"])):
+        with pytest.raises(ValueError):
+            c.prefill(**dict(good, **bad))
+    assert called == []
