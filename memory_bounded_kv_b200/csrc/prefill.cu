@@ -115,10 +115,9 @@ kvb_status launch_bwd(const kvb::PrefillParams& p, cudaStream_t st) {
         return KVB_EINVAL;
     slots = resident_ctas(kk, SK::NT, SK::SMEM);
     if (slots <= 0) return KVB_ECUDA;
-    kvb::PrefillParams s = p;
-    s.pieces = std::min(slots, kvb::kMaxPieces);
-    if (launch_pdl(kk, dim3(s.pieces), dim3(SK::NT), SK::SMEM, st, s, mq, mo, mk, mv) != KVB_OK) return KVB_ECUDA;
-    return launch_pdl(kvb::prefill_dkv_sum_kernel<D, BETA>, dim3(s.pieces, 8), dim3(256), 0, st, s);
+    grid = std::min(slots, kvb::kMaxPieces);
+    if (launch_pdl(kk, dim3(grid), dim3(SK::NT), SK::SMEM, st, p, mq, mo, mk, mv) != KVB_OK) return KVB_ECUDA;
+    return launch_pdl(kvb::prefill_dkv_sum_kernel<D, BETA>, dim3(grid, 2 * D / 16), dim3(256), 0, st, p);
 }
 
 template <int D>
@@ -142,7 +141,7 @@ kvb_status kvb_prefill_attn(const kvb_prefill_args* a, kvb_stream stream) {
 
 size_t kvb_prefill_attn_bwd_workspace_bytes(int32_t T, int32_t Hq) {
     if (T < 1 || Hq < 1) return 0;
-    return round256((size_t)T * Hq * sizeof(float)) + (size_t)kvb::kMaxPieces * 2 * kvb::kPartFloats * sizeof(float);
+    return round256((size_t)T * Hq * sizeof(float)) + (size_t)kvb::kMaxPieces * (2 * kvb::kPartFloats * sizeof(float) + sizeof(int4));
 }
 
 kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* a, const kvb_prefill_grads* g, kvb_stream stream) {
@@ -158,6 +157,7 @@ kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* a, const kvb_prefill_gra
     p.d_o = g->d_o; p.d_lse = g->d_lse; p.dq = g->dq; p.dk = g->dk; p.dv = g->dv; p.dlb = g->d_log_beta;
     p.delta = static_cast<float*>(g->workspace);
     p.parts = p.delta + round256((size_t)a->T * a->Hq * sizeof(float)) / sizeof(float);
+    p.records = reinterpret_cast<int4*>(p.parts + (size_t)kvb::kMaxPieces * 2 * kvb::kPartFloats);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return a->d == 128 ? bwd_dispatch<128>(p, st) : bwd_dispatch<64>(p, st);
 }

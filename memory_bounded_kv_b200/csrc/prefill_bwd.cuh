@@ -677,6 +677,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
             int step = 0, uc = 0;
             bool stop = false;
             long long x = blockIdx.x * piece, round = 0;
+            int4 record = make_int4(0, 0, 0, -1);
             for (;; ++uc) {
                 bool end;
                 int s = 0, len = 0, g = 0, pre = 0, j0 = 0, b0 = 0, b1 = 0, part = 0;
@@ -691,6 +692,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         b1 = u.b0 + (int)(till - u.begin);
                         // a whole key block (0), one that began in an earlier piece (1), one that goes on in the next (2)
                         part = x > u.begin ? 1 : (till < u.end ? 2 : 0);
+                        if (part == 2) record = make_int4(s + j0, min(len - j0, KT), g, (int)((u.end - 1) / piece));
                         x = till;
                     }
                 } else {
@@ -752,6 +754,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 }
                 if (stop) break;
             }
+            if (lane == 0) p.records[blockIdx.x] = record;
             if (stop && lane == 0) fail();
         } else if (warp >= 10) {
             // ======================= extra columns, row values, rows past a document's end =======================
@@ -1159,39 +1162,34 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
 }
 
 // The key blocks that a cut goes through: the sums of their pieces, in order. blockIdx.x names the piece that
-// holds a key block's first step and not its last; a thread sums one key's 2 D / 16 columns (the parts are
+// holds a key block's first step and not its last; a thread sums one key's 8 columns of dV or dK (the parts are
 // [column][key], so that a warp's accesses are whole lines).
 template <int D, bool BETA>
 __global__ void __launch_bounds__(256) prefill_dkv_sum_kernel(const __grid_constant__ PrefillParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const StepLine line(p);
-    const long long piece = line.piece(p.pieces), x0 = blockIdx.x * piece, x1 = x0 + piece;
-    if (!line.cut(p.pieces) || x1 >= line.steps) return;
-    const StepLine::At u = line.find(x1 - 1);
-    if (u.end == x1 || u.begin < x0) return;
-    const int till = (int)((u.end - 1) / piece);   // the last piece with a part of it
-    const int r = threadIdx.x & 127, j = u.kb * 128 + r;
-    constexpr int W = 2 * D / 16;
-    const int col = (blockIdx.y * 2 + (threadIdx.x >> 7)) * W;   // of dV's D columns, then dK's
-    const int at = (col < D ? col : 128 + col - D) * 128 + r;
-    float sum[W];
+    const int4 rec = p.records[blockIdx.x];
+    const int r = threadIdx.x & 127;
+    if (rec.w < 0 || r >= rec.y) return;
+    const int col = (blockIdx.y * 2 + (threadIdx.x >> 7)) * 8;   // of dV's D columns, then dK's
+    const float* first = p.parts + ((size_t)blockIdx.x * 2 + 1) * kPartFloats;
+    const float* others = p.parts + (size_t)blockIdx.x * 2 * kPartFloats;   // + 2 q kPartFloats: the q-th piece after
+    const int at = (col < D ? col : 128 + col - D) * 128 + r, more = rec.w - blockIdx.x;
+    float sum[8];
 #pragma unroll
-    for (int c = 0; c < W; ++c) sum[c] = p.parts[((size_t)blockIdx.x * 2 + 1) * kPartFloats + at + c * 128];
-    for (int q = blockIdx.x + 1; q <= till; ++q)
+    for (int c = 0; c < 8; ++c) sum[c] = first[at + c * 128];
+#pragma unroll 4
+    for (int q = 1; q <= more; ++q)
 #pragma unroll
-        for (int c = 0; c < W; ++c) sum[c] += p.parts[(size_t)q * 2 * kPartFloats + at + c * 128];
-    if (j >= u.d.len) return;
-    const size_t row = (size_t)(u.d.s + j) * p.Hkv + u.g;
+        for (int c = 0; c < 8; ++c) sum[c] += others[(size_t)q * 2 * kPartFloats + at + c * 128];
+    const size_t row = (size_t)(rec.x + r) * p.Hkv + rec.z;
     const float f = col < D ? 1.f : p.scale;
-    uint4* dst = reinterpret_cast<uint4*>((col < D ? p.dv : p.dk) + row * D + (col < D ? col : col - D));
-#pragma unroll
-    for (int c = 0; c < W; c += 8)
-        dst[c / 8] = make_uint4(pack_bf16(sum[c] * f, sum[c + 1] * f), pack_bf16(sum[c + 2] * f, sum[c + 3] * f),
-                                pack_bf16(sum[c + 4] * f, sum[c + 5] * f), pack_bf16(sum[c + 6] * f, sum[c + 7] * f));
+    *reinterpret_cast<uint4*>((col < D ? p.dv + row * D + col : p.dk + row * D + col - D)) =
+        make_uint4(pack_bf16(sum[0] * f, sum[1] * f), pack_bf16(sum[2] * f, sum[3] * f), pack_bf16(sum[4] * f, sum[5] * f),
+                   pack_bf16(sum[6] * f, sum[7] * f));
     if (BETA && col == 0) {
-        float b = p.parts[((size_t)blockIdx.x * 2 + 1) * kPartFloats + 2 * 128 * 128 + r];
-        for (int q = blockIdx.x + 1; q <= till; ++q) b += p.parts[(size_t)q * 2 * kPartFloats + 2 * 128 * 128 + r];
+        float b = first[2 * 128 * 128 + r];
+        for (int q = 1; q <= more; ++q) b += others[(size_t)q * 2 * kPartFloats + 2 * 128 * 128 + r];
         p.dlb[row] = b;
     }
 }

@@ -27,7 +27,7 @@ struct PrefillParams {
     uint16_t* dv;             // [T, Hkv, d]
     float* dlb;               // [T, Hkv] or null
     float* parts;             // [pieces][2] sums of key blocks that a cut goes through (kPartFloats each)
-    int pieces;
+    int4* records;            // [pieces] the key block that goes on behind a piece: first row, rows, kv head, last piece (-1: none)
 };
 
 constexpr int kMaxPieces = 160;                          // CTAs of the kernel by keys, at most
