@@ -304,6 +304,103 @@ def test_more_documents_than_a_warp():
     check_grads(backward(c, o, lse), r)
 
 
+@pytest.mark.parametrize("softcap,pre", [(0.0, False), (4.0, True)])
+def test_many_documents_of_unequal_length(softcap, pre):
+    """More key blocks than the device has SMs, so that whole ones are dealt out (few ones are cut)."""
+    g = np.random.default_rng(16)
+    n = g.integers(0, 400, 60)
+    cu = np.r_[1, 1 + np.cumsum(n)].tolist()
+    prefix = g.integers(0, 300, 60).tolist() if pre else None
+    c = make(16, cu, cu[-1] + 5, 8, 4, 64, grads=True, d_lse=True)
+    o, lse = forward(c, prefix, softcap)
+    r = reference(c, prefix, softcap)
+    check_state(o, lse, r)
+    check_grads(backward(c, o, lse, prefix, softcap), r)
+    assert kvb.kvb_get_error() == 0
+
+
+@pytest.mark.parametrize("beta,d,Hq,Hkv,L", [(True, 128, 4, 1, 2500), (False, 64, 2, 2, 2111), (True, 64, 8, 1, 1400)])
+def test_long_document(beta, d, Hq, Hkv, L):
+    """One document of many tiles: far biases, a moving maximum, key blocks cut into many pieces."""
+    c = make(17, [0, L], L, Hq, Hkv, d, beta, grads=True)
+    if beta:
+        c["lb"][::7] = -1e-4   # tokens that are still seen at the far end
+    o, lse = forward(c)
+    r = reference(c)
+    check_state(o, lse, r)
+    check_grads(backward(c, o, lse), r)
+
+
+def test_growing_weights():
+    """log beta > 0 (the far keys weigh most): the running maximum moves in every tile."""
+    c = make(18, [0, 700], 700, 4, 2, 128, grads=True)
+    c["lb"] = c["lb"].abs() * 0.25
+    o, lse = forward(c)
+    r = reference(c)
+    check(o, r["o"], REL, "o")
+    # logits up to some hundreds: an fp32 sum of that size
+    np.testing.assert_allclose(f64(lse), r["lse"], rtol=2e-6, atol=1e-4)
+
+
+@pytest.mark.parametrize("scale", [0.02, 0.6])
+def test_given_scale(scale):
+    c = make(19, [0, 129, 400], 400, 4, 2, 64, grads=True)
+    o, lse = forward(c, scale=scale)
+    r = reference(c, scale=scale)
+    check(o, r["o"], REL, "o")
+    # scores of about 8 * 0.6 / 0.125 partial sums: the tolerance of scores grows with the scale
+    np.testing.assert_allclose(f64(lse), r["lse"], rtol=2e-6, atol=4e-6 * max(1.0, scale / 0.125))
+    g = backward(c, o, lse, scale=scale)
+    for n in ("dq", "dk", "dv"):
+        check(g[n], r[n], REL, n)
+    check(g["d_log_beta"], r["d_log_beta"], 2e-5 * max(1.0, scale / 0.125), "d_log_beta")
+
+
+def test_without_lse_and_two_streams_at_once():
+    T, Hq, Hkv, d = 900, 8, 2, 128
+    a, b = make(20, [0, 400, 900], T, Hq, Hkv, d), make(21, [0, 900], T, Hq, Hkv, d)
+    want_a, want_b = forward(a)[0], forward(b)[0]
+    oa, ob = torch.zeros_like(want_a), torch.zeros_like(want_b)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        kvb.kvb_prefill_attn(a["q"], a["k"], a["v"], a["lb"], a["cu"], oa, stream=s1)
+        kvb.kvb_prefill_attn(b["q"], b["k"], b["v"], b["lb"], b["cu"], ob, stream=s2.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, want_a) and torch.equal(ob, want_b)
+
+
+def test_gradients_on_two_streams_with_a_workspace_each():
+    T, Hq, Hkv, d = 600, 8, 2, 64
+    cs = [make(22 + k, [0, 250, 600], T, Hq, Hkv, d, grads=True) for k in range(2)]
+    states = [forward(c) for c in cs]
+    want = [backward(c, *s) for c, s in zip(cs, states)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    ws = [torch.empty(kvb.kvb_prefill_attn_bwd_workspace_bytes(T, Hq), dtype=torch.uint8, device="cuda") for _ in cs]
+    got = [{n: torch.zeros_like(x) for n, x in w.items()} for w in want]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, (o, lse), s, w, g in zip(cs, states, streams, ws, got):
+            kvb.kvb_prefill_attn_bwd(c["q"], c["k"], c["v"], c["lb"], c["cu"], o, lse, c["d_o"], None, g["dq"], g["dk"],
+                                     g["dv"], g["d_log_beta"], w, stream=s)
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w[n], g[n]) for n in w)
+
+
+def test_single_tokens_have_no_score_gradient():
+    """A document of one token: softmax is 1, so dq = dk = d_log_beta = 0 and dv = sum of d_o."""
+    T, Hq, Hkv, d = 5, 4, 2, 64
+    c = make(24, list(range(T + 1)), T, Hq, Hkv, d, grads=True)
+    o, lse = forward(c)
+    g = backward(c, o, lse)
+    # p = exp(s - lse) is off by 2^-21 relative, so dS by that of dP (at most 40 here), times 40 of k or q
+    for n in ("dq", "dk"):
+        assert float(g[n].abs().max()) <= 40 * 40 * 2.0 ** -21, n
+    assert torch.all(g["d_log_beta"] == 0)
+    check(g["dv"], reference(c)["dv"], REL, "dv")
+
+
 def test_empty_calls():
     c = make(15, [0, 0, 0], 5, 2, 1, 64, grads=True)
     o, lse = forward(c)
