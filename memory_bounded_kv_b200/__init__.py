@@ -651,34 +651,33 @@ def kvb_paged_compact_blocks(pool, rm_start, rm_len, *, stream=None) -> None:
 # prompts: attention over packed documents, its gradients, and whole prompts into a paged cache
 # ----------------------------------------------------------------------------------------------
 
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_BF16, _F32, _I32, _U8, _Tensor = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.Tensor
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a stream object costs a microsecond
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _is(x, dtype, shape, name, contiguous=True):
     """Raise unless x is a tensor of `dtype` and `shape` (and contiguous). Devices are checked later."""
-    if not isinstance(x, torch.Tensor):
+    if isinstance(x, _Tensor) and x.dtype is dtype and x.shape == shape and (not contiguous or x.is_contiguous()):
+        return
+    if not isinstance(x, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if x.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
     if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if contiguous and not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _one_device(*tensors):
     """The index of the CUDA device that all the tensors (those not None) are on."""
-    dev = tensors[0].get_device()
-    for x in tensors:
-        if x is None:
-            continue
-        d = x.get_device()
-        if d < 0:
-            raise TypeError("every tensor must be a CUDA tensor")
-        if d != dev:
-            raise ValueError(f"tensors on different devices: cuda:{dev} and cuda:{d}")
-    return dev
+    devices = {x.get_device() for x in tensors if x is not None}
+    dev = min(devices)
+    if len(devices) == 1 and dev >= 0:
+        return dev
+    if dev < 0:
+        raise TypeError("every tensor must be a CUDA tensor")
+    raise ValueError("tensors on different devices: " + ", ".join(f"cuda:{d}" for d in sorted(devices)))
 
 
 def _launch(dev, stream, where, call, *args):
@@ -687,7 +686,7 @@ def _launch(dev, stream, where, call, *args):
         s = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
     else:
         s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = call(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -705,8 +704,8 @@ def _packed_strides(x, T, H, d, name):
 
 
 def _kv_strides(k, v, T, H, d):
-    ks, vs = _packed_strides(k, T, H, d, "k"), _packed_strides(v, T, H, d, "v")
-    if ks != vs:
+    ks = _packed_strides(k, T, H, d, "k")
+    if v.stride() != k.stride() and _packed_strides(v, T, H, d, "v") != ks:
         raise ValueError("k and v need equal strides")
     return ks
 
@@ -719,15 +718,17 @@ def _lb_strides(log_beta, T, H):
 
 
 def _prefill_shapes(q, k, cu):
-    for name, x, n in (("q", q, 3), ("k", k, 3), ("cu", cu, 1)):
-        if not isinstance(x, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if x.dim() != n:
-            raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d], cu [N + 1]")
-    if cu.shape[0] < 1:
+    try:
+        T, Hq, d = q.shape
+        _, Hkv, _ = k.shape
+        N, = cu.shape
+    except ValueError:
+        raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d], cu [N + 1]") from None
+    except AttributeError:
+        raise TypeError("q, k and cu must be torch.Tensors") from None
+    if N < 1:
         raise ValueError("cu must be [N + 1]")
-    T, Hq, d = q.shape
-    return T, Hq, k.shape[1], d, cu.shape[0] - 1
+    return T, Hq, Hkv, d, N - 1
 
 
 def _prefill_args(sizes, q, k, v, log_beta, cu, prefix_len, o, lse, scale, softcap):
