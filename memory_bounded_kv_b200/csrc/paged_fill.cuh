@@ -18,11 +18,48 @@ struct PagedPlanParams {
 
 __device__ __forceinline__ int pages_of(int slots) { return (slots + kPageSlots - 1) / kPageSlots; }
 
+// Table entries of the new pages and the slots of the new tokens of a (sequence, kv head), by threads part,
+// part + parts, ... A token's page is read where it stands before the call (the free stack or the table), so
+// nothing waits for these writes themselves.
+__device__ __forceinline__ void paged_row_slots(const PagedPlanParams& p, int bg, int part, int parts) {
+    const PagedCache& c = p.c;
+    const int b = bg / c.Hkv, g = bg % c.Hkv;
+    const int4 call = p.rec[(size_t)p.B * c.Hkv], r = p.rec[bg];
+    const int fresh = r.y;
+    int* map = p.slot_map + (size_t)g * p.T + p.cu[b];
+    if (!r.w) {
+        for (int i = part; i < fresh; i += parts) map[i] = -1;
+        return;
+    }
+    int* table = c.table + (size_t)bg * c.max_pages;
+    const int old_pages = pages_of(r.x), new_pages = pages_of(r.x + fresh);
+    const int* stack = c.free_pages + call.x - 1 - r.z;   // the first new page; the others lie below it
+    for (int j = old_pages + part; j < new_pages; j += parts) table[j] = stack[old_pages - j];
+#pragma unroll 4
+    for (int i = part; i < fresh; i += parts) {
+        const int slot = r.x + i, j = slot / kPageSlots;
+        const int pg = j < old_pages ? table[j] : stack[old_pages - j];
+        int row = -1;
+        if (pg >= 0 && pg < c.num_pages)
+            row = pg * kPageSlots + slot % kPageSlots;
+        else
+            raise_error(KVB_DERR_RANGE);
+        map[i] = row;
+    }
+}
+
+// cu out of order: no token gets a slot
+__device__ __forceinline__ void paged_no_slots(const PagedPlanParams& p, long long at, long long threads) {
+    for (long long i = at; i < (long long)p.c.Hkv * p.T; i += threads) p.slot_map[i] = -1;
+}
+
 // Pages and records of every (sequence, kv head), in order: one CTA, a running sum over the
 // sequences, NT at a time (thread = sequence). A sequence is served when the pages of all
 // sequences up to it fit the free stack, or when it needs none; the pages come off the top of the
 // stack in the order (sequence, kv head, page). Bound by latency: the lengths load eight heads at a time.
-template <int NT>
+// With SLOTS the CTA goes on to the slots itself, a warp per row (few tokens: the second launch would cost
+// more than it spreads).
+template <int NT, bool SLOTS>
 __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ PagedPlanParams p) {
     __shared__ int s_warp[NT / 32];
     __shared__ int s_taken;
@@ -44,7 +81,10 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
         p.rec[rows] = make_int4(avail, !bad, 0, 0);
         s_taken = 0;
     }
-    if (bad) return;
+    if (bad) {
+        if (SLOTS) paged_no_slots(p, tid, NT);
+        return;
+    }
     int ahead = 0;   // pages wanted by the sequences of the earlier rounds
     for (int b0 = 0; b0 < p.B; b0 += NT) {
         const int b = b0 + tid;
@@ -113,44 +153,20 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
         __syncthreads();
     }
     if (tid == 0) *c.free_count = avail - s_taken;
+    if (SLOTS)
+        for (size_t bg = warp; bg < rows; bg += NT / 32) paged_row_slots(p, (int)bg, lane, 32);
 }
 
-// Table entries of the new pages and the slots of the new tokens: blockIdx.x = (sequence, kv head),
-// blockIdx.y strides over its tokens. A token's page is read where it stands before the call (the free
-// stack or the table), so nothing waits for this kernel's own writes.
+// The slots as a launch of their own: blockIdx.x = (sequence, kv head), blockIdx.y strides over its tokens.
 template <int NT>
 __global__ void __launch_bounds__(NT) paged_slots_kernel(const __grid_constant__ PagedPlanParams p) {
-    const PagedCache& c = p.c;
-    const int bg = blockIdx.x, b = bg / c.Hkv, g = bg % c.Hkv, part = blockIdx.y * NT + threadIdx.x, parts = gridDim.y * NT;
+    const int part = blockIdx.y * NT + threadIdx.x, parts = gridDim.y * NT;
     griddep_wait();
     griddep_launch_dependents();
-    const int4 call = p.rec[(size_t)p.B * c.Hkv], r = p.rec[bg];
-    const int start = p.cu[b];
-    if (!call.y) {   // cu out of order: no token gets a slot
-        for (long long i = (long long)bg * parts + part; i < (long long)c.Hkv * p.T; i += (long long)gridDim.x * parts)
-            p.slot_map[i] = -1;
-        return;
-    }
-    const int fresh = r.y;
-    int* map = p.slot_map + (size_t)g * p.T + start;
-    if (!r.w) {
-        for (int i = part; i < fresh; i += parts) map[i] = -1;
-        return;
-    }
-    int* table = c.table + (size_t)bg * c.max_pages;
-    const int old_pages = pages_of(r.x), new_pages = pages_of(r.x + fresh);
-    const int* stack = c.free_pages + call.x - 1 - r.z;   // the first new page; the others lie below it
-    for (int j = old_pages + part; j < new_pages; j += parts) table[j] = stack[old_pages - j];
-#pragma unroll 4
-    for (int i = part; i < fresh; i += parts) {
-        const int slot = r.x + i, j = slot / kPageSlots;
-        const int pg = j < old_pages ? table[j] : stack[old_pages - j];
-        int row = -1;
-        if (pg >= 0 && pg < c.num_pages)
-            row = pg * kPageSlots + slot % kPageSlots;
-        else
-            raise_error(KVB_DERR_RANGE);
-        map[i] = row;
+    if (p.rec[(size_t)p.B * p.c.Hkv].y) {
+        paged_row_slots(p, blockIdx.x, part, parts);
+    } else {
+        paged_no_slots(p, (long long)blockIdx.x * parts + part, (long long)gridDim.x * parts);
     }
 }
 

@@ -174,7 +174,11 @@ kvb_status kvb_paged_plan(const kvb_paged_cache* c, const int32_t* cu, int32_t T
     if (!workspace || !aligned16(workspace) || workspace_bytes < kvb_paged_plan_workspace_bytes(c->B, c->Hkv)) return KVB_EINVAL;
     kvb::PagedPlanParams p{pc, cu, slot_map, c->B, T, empty_only, static_cast<int4*>(workspace)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (launch_pdl(kvb::paged_plan_kernel<1024>, dim3(1), dim3(1024), 0, st, p) != KVB_OK) return KVB_ECUDA;
+    // few slots: the second launch costs more than it spreads (200 tokens, 2 heads: 7.2 -> 6.2 us with the caller's
+    // two copies; 131072 tokens, 8 heads need it)
+    if ((long long)T * c->Hkv <= 4096)
+        return launch_pdl(kvb::paged_plan_kernel<1024, true>, dim3(1), dim3(1024), 0, st, p);
+    if (launch_pdl(kvb::paged_plan_kernel<1024, false>, dim3(1), dim3(1024), 0, st, p) != KVB_OK) return KVB_ECUDA;
     // a block for every 1024 tokens of a row's share (256 tokens: 16.7 us instead of 13 for 131072 tokens in 256 rows)
     const long long share = ((long long)T / c->B + 1023) / 1024;
     const unsigned parts = (unsigned)std::min<long long>(std::max<long long>(share, 1), 64);

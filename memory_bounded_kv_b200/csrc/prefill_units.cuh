@@ -176,8 +176,8 @@ struct StepLine {
     __device__ __forceinline__ long long piece(int pieces) const { return (steps + pieces - 1) / pieces; }
     // Whether to cut: where one key block weighs as much as three quarters of a CTA's share. Below that whole
     // key blocks, heaviest first, balance as well, and CTAs that walk the same queries together read them from
-    // L2 (8192 tokens, 32/8 heads, d 128: 895 us whole, 972 and the sums cut; 5003 ragged tokens, 16/4 heads,
-    // with a cap: all three kernels 461 us whole, 384 cut).
+    // L2 (8192 tokens, 32/8 heads, d 128: 895 us whole, 972 and the sums cut). 5003 ragged tokens, 16/4 heads,
+    // d 128, with a cap, all kernels: 461 us whole, 384 cut; 301 tokens, 8/2 heads, d 64: 44.6 whole, 37.7 cut.
     __device__ __forceinline__ bool cut(int pieces) const { return 4LL * longest > 3 * piece(pieces); }
 
     struct At {
