@@ -323,14 +323,24 @@ __device__ __forceinline__ void store_bf16x32(void* dst, const float (&o)[32], f
 // tanh(y) = 1 - 2 / (1 + e^2y): off by about 2^-23 absolute
 __device__ __forceinline__ float tanh_exp(float y) { return 1.f - 2.f * rcp_approx(1.f + ex2_approx(2.f * kLog2e * y)); }
 
-// x = amp tanh(per_cap x), 32 values: where a warp's values all lie in [-1/2, 1/2] (scores small beside the
-// cap, the common case) by y times the polynomial of degree 4 in y^2 whose largest relative error is
-// smallest (1.3e-8), which also keeps small values to fp32 accuracy; else through the exponential.
+// x = amp tanh(per_cap x), 32 values: where a warp's y = per_cap x are small (scores small beside the cap, the
+// common case) by y times the polynomial in y^2 whose largest relative error is smallest, which also keeps
+// small values to fp32 accuracy: degree 2 for y^2 <= 1/32 (5e-8; a warp's 1024 scores of variance 1 beside a
+// cap of 20), with per_cap in the coefficients, degree 4 for y^2 <= 1/4 (1.3e-8); else through the exponential.
 __device__ __forceinline__ void cap_scores(float* x, float per_cap, float amp) {
     float most = 0.f;
 #pragma unroll
     for (int c = 0; c < 32; c += 2) most = max3(most, fabsf(x[c]), fabsf(x[c + 1]));
-    if (__all_sync(kFull, most * per_cap <= 0.5f)) {
+    const float k1 = amp * per_cap, k2 = per_cap * per_cap;
+    // the coefficients' range: per_cap^4 and x^2 stay normal numbers
+    if (__all_sync(kFull, most * per_cap <= 0.17677669f) && per_cap >= 1e-6f && per_cap <= 1e6f) {
+        const uint64_t c2 = same2(k1 * k2 * k2 * 0.13083961606025696f), c1 = same2(k1 * k2 * -0.333304226398468f), c0 = same2(k1);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const uint64_t z = pk2(x[c], x[c + 1]), u = mul2(z, z);
+            upk2(mul2(fma2(fma2(c2, u, c1), u, c0), z), x[c], x[c + 1]);
+        }
+    } else if (__all_sync(kFull, most * per_cap <= 0.5f)) {
         const uint64_t c4 = same2(amp * 0.017135005444288254f), c3 = same2(amp * -0.05298607423901558f),
                        c2 = same2(amp * 0.13324779272079468f), c1 = same2(amp * -0.3333306908607483f), c0 = same2(amp);
 #pragma unroll
