@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 for (int c = 0; c < 64; c += 2) {
                     float u, v;
                     upk2(fma2(pk2(x[c], x[c + 1]), c2, n2), u, v);
-                    if ((D == 64 || CAP) && c % 8 == 6) {   // a quarter of the exponentials on the FMA pipe, as forward
+                    if (D == 64 && c % 8 == 6) {   // a quarter of the exponentials on the FMA pipe, as forward
                         exp2_poly2<5>(u, v);
                     } else {
                         u = ex2_approx(u);
@@ -1021,7 +1021,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     for (int e = 0; e < 32; e += 2) {
                         float a, b;
                         upk2(CAP ? pk2(x[c0 + e], x[c0 + e + 1]) : mul2(pk2(x[c0 + e], x[c0 + e + 1]), c2), a, b);
-                        if ((D == 64 || CAP) && e % 8 == 6) {   // a quarter of the exponentials on the FMA pipe, as forward
+                        if (D == 64 && e % 8 == 6) {   // a quarter of the exponentials on the FMA pipe, as forward
                             exp2_poly2<5>(a, b);
                         } else {
                             a = ex2_approx(a);

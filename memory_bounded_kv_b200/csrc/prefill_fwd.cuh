@@ -472,10 +472,10 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                     for (int e = 0; e < 32; e += 2) {
                         float a, b;
                         upk2(fma2(pk2(x[c + e], x[c + e + 1]), c2, n2), a, b);
-                        // a quarter of the exponentials on the FMA pipe, where exponentials bound the kernel (d 64:
-                        // 388 -> 371 us, with a cap 1014 -> 978 us at d 128); plain d 128 is held by the products
-                        // and the power cap, where it costs (454 -> 466 us; 8192 tokens, 32/8 heads)
-                        if ((D == 64 || CAP) && e % 8 == 6) {
+                        // a quarter of the exponentials on the FMA pipe, where exponentials bound the kernel (d 64: 388 ->
+                        // 371 us, with a cap 874 -> 842); at d 128 the products and the power cap hold it and that costs
+                        // or changes nothing (454 -> 466 us, with a cap 823 -> 825; 8192 tokens, 32/8 heads)
+                        if (D == 64 && e % 8 == 6) {
                             exp2_poly2<4>(a, b);
                         } else {
                             a = ex2_approx(a);
