@@ -10,7 +10,7 @@
 // (2^-9 relative), which d log beta, an fp32 result whose terms cancel, would show. The first kernel
 // starts from that estimate e_i = dO . o - dlse_i; its row sums of dS are then sum_j p_ij dP_ij - e_i,
 // so e_i + their sum - dlse_i is delta to fp32, for one addition per score. dq, held in bf16 itself,
-// keeps the estimate.
+// keeps the estimate, but for rows whose keys fit one tile.
 //
 // What bounds both is shared memory and the hand-over between products and softmax. A product of two
 // shared-memory operands reads 16 (128 + N) x 2 bytes per K step of 16: at N = 64 that is 48 clocks of
@@ -26,6 +26,8 @@
 // adds up the few that a cut goes through.
 //   The two warpgroups share a tile: each takes 64 of its 128 columns, a thread per row.
 // The bias rides the S product as in prefill_fwd_kernel; by keys, - lse and - delta ride S and dP too.
+// One document of 8192 tokens, 32/8 heads, d 128: by query rows 690 us (3 products, 1.2 PFLOP/s), by keys
+// 890 us (4 products, 1.24 PFLOP/s), both near the power cap in long runs; d 64 560 and 630 us.
 #pragma once
 
 #include "prefill_units.cuh"

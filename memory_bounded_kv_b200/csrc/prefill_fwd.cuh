@@ -23,6 +23,16 @@
 // but 0 times a neighbour's NaN is not).
 // Every wait is bounded (wait_ns); a CTA that gives up records KVB_DERR_TIMEOUT and lets its copies
 // and products finish (bounded); the rows that it had not written keep what they held.
+//
+// What bounds it: a K/V step of the pair is 2174 clocks of products (see prefill_bwd.cuh for their rates)
+// and takes some 3400, the rest being the hand-over between products and softmax: a tile's next S waits
+// for its P V, because two S and two O fill the tensor memory. One document of 8192 tokens, 32/8 heads,
+// d 128: 435 us (1.26 PFLOP/s) in short bursts, 501 us at the power cap; d 64 371 us (exponentials); with
+// capped scores 830 us. Short documents pay a near tile and 2.5k clocks of output a unit: 6151 tokens in
+// 24 documents 59 us. One issuing warp, not one per tile: with two, both tiles' products interleave and
+// both finish late (475 -> 537 us). Pairs always: a tile alone takes 0.83 of a pair's step, so units of
+// one tile lose even where the longest pair holds up the rest (4000 tokens in 5 documents, 16/2 heads, d 64,
+// with a cap: 52.6 -> 69.5 us).
 #pragma once
 
 #include "prefill_units.cuh"
@@ -148,234 +158,235 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
 
     // a row of 128 scores and its packed weights want more than the launch's 168 registers a thread
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REG_REST));
-    if (warp == 9) {
-        // ======================= units and loads =======================
-        const PrefillWalk walk(p, sh);
-        const long long units = walk.units;
-        int step = 0, uc = 0;
-        bool stop = false;
-        for (long long r = 0; !stop; ++r, ++uc) {
-            // rounds of the units: one past the last ends (an odd round may hold this CTA's unit or not)
-            const long long u = PrefillWalk::nth(r, blockIdx.x, gridDim.x);
-            const bool end = r * gridDim.x >= units;
-            if (!end && u >= units) { --uc; continue; }
-            PrefillUnit x{};
-            int n0 = 0, n1 = 0;
-            if (!end) {
-                x = walk.unit(u);
-                const int bt = 1 << (sh - 1), i0 = x.blk << sh, i1 = i0 + bt;
-                n0 = (max(min(i1, x.len), x.pre) + KT - 1) / KT;
-                n1 = i1 < x.len ? (max(min(i1 + bt, x.len), x.pre) + KT - 1) / KT : 0;
-            }
-            const int ub = uc & 1;
-            if (uc >= 2 && !warp_wait(&u_empty[ub], (unsigned)((uc >> 1) - 1) & 1u, p.wait_ns)) {
-                if (lane == 0) fail();
-                break;
-            }
-            if (__any_sync(kFull, *s_abort != 0)) break;
-            if (lane == 0) {
-                int* m = info + ub * 8;
-                m[0] = end ? -1 : x.s;
-                m[1] = x.len;
-                m[2] = x.blk << sh;
-                m[3] = x.g;
-                m[4] = x.pre;
-                m[5] = n0;
-                m[6] = n1;
-                mbar_arrive(&u_full[ub]);
-            }
-            __syncwarp();
-            if (end) break;
-            if (uc >= 1 && !warp_wait(q_empty, (unsigned)(uc - 1) & 1u, p.wait_ns)) {
-                if (lane == 0) fail();
-                break;
-            }
-            const int n = max(n0, n1);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, (unsigned)(2 * SH::TILE));
-                for (int t = 0; t < 2; ++t)
-                    for (int h = 0; h < D / 64; ++h)
-                        tma_load_3d(smem + SH::Q_OFF + t * SH::TILE + h * SH::HALF, &tmQ, 64 * h, x.g << lg,
-                                    x.s + (x.blk << sh) + (t << (sh - 1)), q_full);
-                s_steps[1] = uc + 1;
-            }
-            for (int tile = n - 1; tile >= 0; --tile, ++step) {
-                const int st = step % ST;
-                const unsigned ph = (unsigned)((step / ST) - 1) & 1u;
-                if (step >= ST && !warp_wait(&k_empty[st], ph, p.wait_ns)) { stop = true; break; }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REG_REST));
+        if (warp == 9) {
+            // ======================= units and loads =======================
+            const PrefillWalk walk(p, sh);
+            const long long units = walk.units;
+            int step = 0, uc = 0;
+            bool stop = false;
+            for (long long r = 0; !stop; ++r, ++uc) {
+                // rounds of the units: one past the last ends (an odd round may hold this CTA's unit or not)
+                const long long u = PrefillWalk::nth(r, blockIdx.x, gridDim.x);
+                const bool end = r * gridDim.x >= units;
+                if (!end && u >= units) { --uc; continue; }
+                PrefillUnit x{};
+                int n0 = 0, n1 = 0;
+                if (!end) {
+                    x = walk.unit(u);
+                    const int bt = 1 << (sh - 1), i0 = x.blk << sh, i1 = i0 + bt;
+                    n0 = (max(min(i1, x.len), x.pre) + KT - 1) / KT;
+                    n1 = i1 < x.len ? (max(min(i1 + bt, x.len), x.pre) + KT - 1) / KT : 0;
+                }
+                const int ub = uc & 1;
+                if (uc >= 2 && !warp_wait(&u_empty[ub], (unsigned)((uc >> 1) - 1) & 1u, p.wait_ns)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                if (__any_sync(kFull, *s_abort != 0)) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&k_full[st], (unsigned)SH::TILE);
-                    for (int h = 0; h < D / 64; ++h)
-                        tma_load_3d(smem + SH::K_OFF + st * SH::TILE + h * SH::HALF, &tmK, 64 * h, x.g, x.s + tile * KT, &k_full[st]);
-                    s_steps[0] = step + 1;
+                    int* m = info + ub * 8;
+                    m[0] = end ? -1 : x.s;
+                    m[1] = x.len;
+                    m[2] = x.blk << sh;
+                    m[3] = x.g;
+                    m[4] = x.pre;
+                    m[5] = n0;
+                    m[6] = n1;
+                    mbar_arrive(&u_full[ub]);
                 }
-                if (step >= ST && !warp_wait(&v_empty[st], ph, p.wait_ns)) { stop = true; break; }
+                __syncwarp();
+                if (end) break;
+                if (uc >= 1 && !warp_wait(q_empty, (unsigned)(uc - 1) & 1u, p.wait_ns)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                const int n = max(n0, n1);
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&v_full[st], (unsigned)SH::TILE);
-                    for (int h = 0; h < D / 64; ++h)
-                        tma_load_3d(smem + SH::V_OFF + st * SH::TILE + h * SH::HALF, &tmV, 64 * h, x.g, x.s + tile * KT, &v_full[st]);
+                    const int tiles = n1 > 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(q_full, (unsigned)(tiles * SH::TILE));
+                    for (int t = 0; t < tiles; ++t)
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(smem + SH::Q_OFF + t * SH::TILE + h * SH::HALF, &tmQ, 64 * h, x.g << lg,
+                                        x.s + (x.blk << sh) + (t << (sh - 1)), q_full);
+                    s_steps[1] = uc + 1;
                 }
-                if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
+                for (int tile = n - 1; tile >= 0; --tile, ++step) {
+                    const int st = step % ST;
+                    const unsigned ph = (unsigned)((step / ST) - 1) & 1u;
+                    if (step >= ST && !warp_wait(&k_empty[st], ph, p.wait_ns)) { stop = true; break; }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&k_full[st], (unsigned)SH::TILE);
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(smem + SH::K_OFF + st * SH::TILE + h * SH::HALF, &tmK, 64 * h, x.g, x.s + tile * KT, &k_full[st]);
+                        s_steps[0] = step + 1;
+                    }
+                    if (step >= ST && !warp_wait(&v_empty[st], ph, p.wait_ns)) { stop = true; break; }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&v_full[st], (unsigned)SH::TILE);
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(smem + SH::V_OFF + st * SH::TILE + h * SH::HALF, &tmV, 64 * h, x.g, x.s + tile * KT, &v_full[st]);
+                    }
+                    if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
+                }
+                if (stop && lane == 0) fail();
             }
-            if (stop && lane == 0) fail();
-        }
-    } else if (warp >= 10) {
-        // ======================= bias columns, V past a document's end =======================
-        // two warps, a step each in turn; the log betas of a warp's next step load while it writes this one's
-        const float unit_b = CAP ? kLog2e : 1.f / p.scale;
-        int step = 0;
-        bool stop = false;
-        for (int uc = 0; !stop; ++uc) {
-            const int ub = uc & 1;
-            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
-            const int* m = info + ub * 8;
-            const int s = m[0], len = m[1], i0 = m[2], g = m[3], n = max(m[5], m[6]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&u_empty[ub]);
-            if (s < 0) break;
-            float nb[4] = {0.f, 0.f, 0.f, 0.f};
-            auto load = [&](int tile) {
+        } else if (warp >= 10) {
+            // ======================= bias columns, V past a document's end =======================
+            // two warps, a step each in turn; the log betas of a warp's next step load while it writes this one's
+            const float unit_b = CAP ? kLog2e : 1.f / p.scale;
+            int step = 0;
+            bool stop = false;
+            for (int uc = 0; !stop; ++uc) {
+                const int ub = uc & 1;
+                if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
+                const int* m = info + ub * 8;
+                const int s = m[0], len = m[1], i0 = m[2], g = m[3], n = max(m[5], m[6]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&u_empty[ub]);
+                if (s < 0) break;
+                float nb[4] = {0.f, 0.f, 0.f, 0.f};
+                auto load = [&](int tile) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = tile * KT + lane + 32 * e;
-                    nb[e] = tile >= 0 && j < len ? p.lb[(long long)(s + j) * p.lb_st + g * p.lb_sh] : 0.f;
-                }
-            };
-            const int q0 = (step + warp) & 1;   // this warp's first step of the unit
-            if (BETA) load(n - 1 - q0);
-            for (int q = q0; q < n; q += 2) {
-                const int tile = n - 1 - q, k = step + q, st = k % ST;
-                const unsigned ph = (unsigned)(k / ST) & 1u;
-                if (BETA) {
-                    float b[4];
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = tile * KT + lane + 32 * e;
+                        nb[e] = tile >= 0 && j < len ? p.lb[(long long)(s + j) * p.lb_st + g * p.lb_sh] : 0.f;
+                    }
+                };
+                const int q0 = (step + warp) & 1;   // this warp's first step of the unit
+                if (BETA) load(n - 1 - q0);
+                for (int q = q0; q < n; q += 2) {
+                    const int tile = n - 1 - q, k = step + q, st = k % ST;
+                    const unsigned ph = (unsigned)(k / ST) & 1u;
+                    if (BETA) {
+                        float b[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) b[e] = clamp_log_beta(nb[e]) * unit_b;
-                    load(tile - 2);
-                    // the slopes of step k - ST were read before its P V product, which freed the V stage
-                    if (k >= ST && !warp_wait(&v_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
+                        for (int e = 0; e < 4; ++e) b[e] = clamp_log_beta(nb[e]) * unit_b;
+                        load(tile - 2);
+                        // the slopes of step k - ST were read before its P V product, which freed the V stage
+                        if (k >= ST && !warp_wait(&v_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        reinterpret_cast<float*>(smem + SH::LB_OFF)[st * KT + lane + 32 * e] = b[e];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&lb_full[st]);
-                    if (!CAP) {
-                        if (k >= ST && !warp_wait(&k_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<float*>(smem + SH::LB_OFF)[st * KT + lane + 32 * e] = b[e];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&lb_full[st]);
+                        if (!CAP) {
+                            if (k >= ST && !warp_wait(&k_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int c = lane + 32 * e;
-                            *reinterpret_cast<uint4*>(smem + SH::KX_OFF + st * SH::XCOL + plain16_off(c, 0)) =
-                                bias_columns(b[e], i0 - tile * KT - c);
+                            for (int e = 0; e < 4; ++e) {
+                                const int c = lane + 32 * e;
+                                *reinterpret_cast<uint4*>(smem + SH::KX_OFF + st * SH::XCOL + plain16_off(c, 0)) =
+                                    bias_columns(b[e], i0 - tile * KT - c);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&k_full[st]);
+                        }
+                    }
+                    if ((tile + 1) * KT > len) {
+                        if (!warp_wait(&v_full[st], ph, p.wait_ns)) { stop = true; break; }
+                        const int rows = len - tile * KT;
+                        unsigned char* vt = smem + SH::V_OFF + st * SH::TILE;
+                        for (int x = lane; x < (KT - rows) * 8 * (D / 64); x += 32) {
+                            const int row = rows + x / (8 * (D / 64)), c = x % (8 * (D / 64));
+                            *reinterpret_cast<uint4*>(vt + (c >> 3) * SH::HALF + row * 128 + ((c & 7) << 4)) =
+                                make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&k_full[st]);
+                        if (lane == 0) mbar_arrive(&v_fix[st]);
                     }
+                    if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
-                if ((tile + 1) * KT > len) {
-                    if (!warp_wait(&v_full[st], ph, p.wait_ns)) { stop = true; break; }
-                    const int rows = len - tile * KT;
-                    unsigned char* vt = smem + SH::V_OFF + st * SH::TILE;
-                    for (int x = lane; x < (KT - rows) * 8 * (D / 64); x += 32) {
-                        const int row = rows + x / (8 * (D / 64)), c = x % (8 * (D / 64));
-                        *reinterpret_cast<uint4*>(vt + (c >> 3) * SH::HALF + row * 128 + ((c & 7) << 4)) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                step += n;
+            }
+            if (stop && lane == 0) fail();
+        } else if (warp == 8) {
+            // ======================= products =======================
+            // the warp stays together (its values are uniform); one lane issues
+            constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
+            int step = 0;
+            unsigned fixes = 0;           // bit st: parity of the next clearing of stage st
+            unsigned pc = 0;              // bit t: parity of tile t's next P
+            int oc0 = 0, oc1 = 0;
+            bool stop = false;
+            const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::K_OFF);
+            const uint32_t v_lo = desc_mn_lo(sbase + SH::V_OFF, SH::HALF);
+            const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
+            auto scores = [&](int t, int st, bool past) {
+                const uint32_t ts = tmem + SH::TM_S + t * 128;
+                umma_kmajor<D / 16>(ts, q_lo + t * (SH::TILE >> 4), SH::HALF, k_lo + st * (SH::TILE >> 4), SH::HALF, idesc_s);
+                if (BETA && !CAP && past)
+                    umma_bf16(ts, desc(qx_lo + t * (SH::XCOL >> 4), kDescPlainHi), desc(kx_lo + st * (SH::XCOL >> 4), kDescPlainHi),
+                              idesc_s, 1u);
+                umma_commit(&s_full[t]);
+            };
+            for (int uc = 0; !stop; ++uc) {
+                const int ub = uc & 1;
+                if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
+                const int* m = info + ub * 8;
+                const int s = __shfl_sync(kFull, m[0], 0), len = __shfl_sync(kFull, m[1], 0), i0 = __shfl_sync(kFull, m[2], 0);
+                const int n0 = __shfl_sync(kFull, m[5], 0), n1 = __shfl_sync(kFull, m[6], 0);
+                if (lane == 0) mbar_arrive(&u_empty[ub]);
+                if (s < 0) break;
+                const int n = max(n0, n1), i1 = i0 + (1 << (sh - 1));
+                if (!warp_wait(q_full, (unsigned)uc & 1u, p.wait_ns) ||
+                    !warp_wait(&k_full[step % ST], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                tc_fence_after();
+                if (elect_one()) {
+                    if (n - 1 < n0) scores(0, step % ST, n * KT <= i0 + 1);
+                    if (n - 1 < n1) scores(1, step % ST, n * KT <= i1 + 1);
+                    umma_commit(&k_empty[step % ST]);
+                    if (n == 1) umma_commit(q_empty);
+                }
+                __syncwarp();
+                for (int tile = n - 1; tile >= 0; --tile, ++step) {
+                    const int st = step % ST, nst = (step + 1) % ST;
+                    const bool more = tile > 0;
+                    if (more && !warp_wait(&k_full[nst], (unsigned)((step + 1) / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                    if (!warp_wait(&v_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+                    if ((tile + 1) * KT > len) {
+                        if (!warp_wait(&v_fix[st], (fixes >> st) & 1u, p.wait_ns)) { stop = true; break; }
+                        fixes ^= 1u << st;
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&v_fix[st]);
-                }
-                if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
-            }
-            step += n;
-        }
-        if (stop && lane == 0) fail();
-    } else if (warp == 8) {
-        // ======================= products =======================
-        // the warp stays together (its values are uniform); one lane issues
-        constexpr uint32_t idesc_s = umma_idesc_bf16(R, KT), idesc_o = umma_idesc_bf16_bmn(R, D);
-        int step = 0;
-        unsigned fixes = 0;           // bit st: parity of the next clearing of stage st
-        unsigned pc = 0;              // bit t: parity of tile t's next P
-        int oc0 = 0, oc1 = 0;
-        bool stop = false;
-        const uint32_t q_lo = desc_sw128_lo(sbase + SH::Q_OFF), k_lo = desc_sw128_lo(sbase + SH::K_OFF);
-        const uint32_t v_lo = desc_mn_lo(sbase + SH::V_OFF, SH::HALF);
-        const uint32_t qx_lo = desc_plain_lo(sbase + SH::QX_OFF), kx_lo = desc_plain_lo(sbase + SH::KX_OFF);
-        auto scores = [&](int t, int st, bool past) {
-            const uint32_t ts = tmem + SH::TM_S + t * 128;
-            umma_kmajor<D / 16>(ts, q_lo + t * (SH::TILE >> 4), SH::HALF, k_lo + st * (SH::TILE >> 4), SH::HALF, idesc_s);
-            if (BETA && !CAP && past)
-                umma_bf16(ts, desc(qx_lo + t * (SH::XCOL >> 4), kDescPlainHi), desc(kx_lo + st * (SH::XCOL >> 4), kDescPlainHi),
-                          idesc_s, 1u);
-            umma_commit(&s_full[t]);
-        };
-        for (int uc = 0; !stop; ++uc) {
-            const int ub = uc & 1;
-            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
-            const int* m = info + ub * 8;
-            const int s = __shfl_sync(kFull, m[0], 0), len = __shfl_sync(kFull, m[1], 0), i0 = __shfl_sync(kFull, m[2], 0);
-            const int n0 = __shfl_sync(kFull, m[5], 0), n1 = __shfl_sync(kFull, m[6], 0);
-            if (lane == 0) mbar_arrive(&u_empty[ub]);
-            if (s < 0) break;
-            const int n = max(n0, n1), i1 = i0 + (1 << (sh - 1));
-            if (!warp_wait(q_full, (unsigned)uc & 1u, p.wait_ns) ||
-                !warp_wait(&k_full[step % ST], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
-            tc_fence_after();
-            if (elect_one()) {
-                if (n - 1 < n0) scores(0, step % ST, n * KT <= i0 + 1);
-                if (n - 1 < n1) scores(1, step % ST, n * KT <= i1 + 1);
-                umma_commit(&k_empty[step % ST]);
-                if (n == 1) umma_commit(q_empty);
-            }
-            __syncwarp();
-            for (int tile = n - 1; tile >= 0; --tile, ++step) {
-                const int st = step % ST, nst = (step + 1) % ST;
-                const bool more = tile > 0;
-                if (more && !warp_wait(&k_full[nst], (unsigned)((step + 1) / ST) & 1u, p.wait_ns)) { stop = true; break; }
-                if (!warp_wait(&v_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
-                if ((tile + 1) * KT > len) {
-                    if (!warp_wait(&v_fix[st], (fixes >> st) & 1u, p.wait_ns)) { stop = true; break; }
-                    fixes ^= 1u << st;
-                }
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int nt = t ? n1 : n0;
-                    const bool have = tile < nt, first = tile == nt - 1;
-                    if (have) {
-                        if (first) {
-                            int& oc = t ? oc1 : oc0;
-                            if (oc > 0 && !warp_wait(&o_empty[t], (unsigned)(oc - 1) & 1u, p.wait_ns)) { stop = true; break; }
-                            ++oc;
-                        }
-                        if (!warp_wait(&p_half[t], (pc >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                        tc_fence_after();
-                        if (elect_one())
-                            umma_rows<KT / 32>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128,
-                                               v_lo + st * (SH::TILE >> 4), idesc_o, first);
-                        __syncwarp();
-                        if (!warp_wait(&p_full[t], (pc >> t) & 1u, p.wait_ns)) { stop = true; break; }
-                        pc ^= 1u << t;
-                    }
-                    tc_fence_after();
-                    if (elect_one()) {
+                    for (int t = 0; t < 2; ++t) {
+                        const int nt = t ? n1 : n0;
+                        const bool have = tile < nt, first = tile == nt - 1;
                         if (have) {
-                            umma_rows<KT / 32>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128 + 32,
-                                               v_lo + st * (SH::TILE >> 4) + 64 * 128 / 16, idesc_o, false);
-                            if (tile == 0) umma_commit(&o_full[t]);
+                            if (first) {
+                                int& oc = t ? oc1 : oc0;
+                                if (oc > 0 && !warp_wait(&o_empty[t], (unsigned)(oc - 1) & 1u, p.wait_ns)) { stop = true; break; }
+                                ++oc;
+                            }
+                            if (!warp_wait(&p_half[t], (pc >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                            tc_fence_after();
+                            if (elect_one())
+                                umma_rows<KT / 32>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128,
+                                                   v_lo + st * (SH::TILE >> 4), idesc_o, first);
+                            __syncwarp();
+                            if (!warp_wait(&p_full[t], (pc >> t) & 1u, p.wait_ns)) { stop = true; break; }
+                            pc ^= 1u << t;
                         }
-                        if (t == 1) umma_commit(&v_empty[st]);
-                        if (more && tile - 1 < nt) scores(t, nst, tile * KT <= (t ? i1 : i0) + 1);
-                        if (t == 1 && more) umma_commit(&k_empty[nst]);
-                        if (t == 1 && tile == 1) umma_commit(q_empty);
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (have) {
+                                umma_rows<KT / 32>(tmem + SH::TM_O + t * 128, tmem + SH::TM_S + t * 128 + 32,
+                                                   v_lo + st * (SH::TILE >> 4) + 64 * 128 / 16, idesc_o, false);
+                                if (tile == 0) umma_commit(&o_full[t]);
+                            }
+                            if (t == 1) umma_commit(&v_empty[st]);
+                            if (more && tile - 1 < nt) scores(t, nst, tile * KT <= (t ? i1 : i0) + 1);
+                            if (t == 1 && more) umma_commit(&k_empty[nst]);
+                            if (t == 1 && tile == 1) umma_commit(q_empty);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (stop) break;
                 }
-                if (stop) break;
             }
+            if (stop && lane == 0) fail();
         }
-        if (stop && lane == 0) fail();
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REG_SOFT));
         // ======================= softmax and output =======================
