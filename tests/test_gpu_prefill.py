@@ -578,3 +578,31 @@ def test_prompts_then_decode(beta):
     cache.prefill(j["q"], j["k"], j["v"], j["lb"], j["cu"], torch.arange(70, dtype=torch.int32).cuda(), oj)
     assert kvb.kvb_get_error() == _lib.DERR_LEN
     assert cache.len.tolist() == [[131] * 2, [70] * 2, [66] * 2]
+
+
+def test_reset_and_prefill_captured_and_replayed():
+    """A graph of reset and prefill: every replay serves the lengths that stand in cu then."""
+    B, Hq, Hkv, d, T = 2, 4, 2, 64, 300
+    cache = PagedKVCache(B, Hq, Hkv, d, max_pages=6, num_pages=16, M=300)
+    c = make(50, [0, 100, 300], T, Hq, Hkv, d)
+    pos = torch.cat([torch.arange(100), torch.arange(200)]).to(torch.int32).cuda()
+    o, lse = torch.zeros(T, Hq, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, Hq, device="cuda")
+
+    def work():
+        cache.reset()
+        cache.prefill(c["q"], c["k"], c["v"], c["lb"], c["cu"], pos, o, lse)
+    work()
+    want = o.clone(), cache.len.clone(), host(cache.pool.k_pages)[host(cache.pool.table)[1, 0, :4]].copy()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for _ in range(2):
+        o.zero_()
+        graph.replay()
+        assert torch.equal(o, want[0]) and torch.equal(cache.len, want[1])
+        np.testing.assert_array_equal(host(cache.pool.k_pages)[host(cache.pool.table)[1, 0, :4]], want[2])
+    c["cu"].copy_(torch.tensor([0, 100, 260], dtype=torch.int32))
+    graph.replay()
+    assert cache.len.tolist() == [[100] * 2, [160] * 2] and cache.pages_in_use() == 2 * (2 + 3)
+    assert kvb.kvb_get_error() == 0
