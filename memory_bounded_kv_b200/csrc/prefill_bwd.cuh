@@ -7,7 +7,7 @@
 //                       d log beta_j = sum_i dS_ij max(i - j, 0) in fp32
 //
 // delta_i = sum_j p_ij dP_ij - dlse_i. dO . o would give it from the output, but o is held in bf16
-// (2^-9 relative), which d log beta, an fp32 result whose terms cancel, would show. The first kernel
+// (2^-8 relative), which d log beta, an fp32 result whose terms cancel, would show. The first kernel
 // starts from that estimate e_i = dO . o - dlse_i; its row sums of dS are then sum_j p_ij dP_ij - e_i,
 // so e_i + their sum - dlse_i is delta to fp32, for one addition per score. dq, held in bf16 itself,
 // keeps the estimate, but for rows whose keys fit one tile.
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                         sum = add2(sum, ds);
                         float u, v;
                         upk2(CAP ? mul2(ds, cap_slope2(th[c0 + e], th[c0 + e + 1], inv_cap2)) : ds, u, v);
-                        w[e / 2] = pack_bf16(u, v);   // dS enters dS K as bf16: 2^-9 each, as dq's own rounding
+                        w[e / 2] = pack_bf16(u, v);   // dS enters dS K as bf16: 2^-8 each, as dq's own rounding
                     }
                     tmem_st16(tl + SH::TM_DP + t * 64 + c0 / 2, w);
                 }
@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                         }
                         x[c0 + e] = a;
                         x[c0 + e + 1] = b;
-                        w[e / 2] = pack_bf16(a, b);   // P and dS enter the gradients' products as bf16: 2^-9 each
+                        w[e / 2] = pack_bf16(a, b);   // P and dS enter the gradients' products as bf16: 2^-8 each
                     }
                     tmem_st16(tl + SH::TM_S + t * 64 + c0 / 2, w);
                     if (SH::SPLIT_P || c0 > 0) {

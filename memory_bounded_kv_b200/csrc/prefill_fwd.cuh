@@ -27,7 +27,7 @@
 // What bounds it: a K/V step of the pair is 2174 clocks of products (see prefill_bwd.cuh for their rates)
 // and takes some 3400, the rest being the hand-over between products and softmax: a tile's next S waits
 // for its P V, because two S and two O fill the tensor memory. One document of 8192 tokens, 32/8 heads,
-// d 128: 435 us (1.26 PFLOP/s) in short bursts, 501 us at the power cap; d 64 371 us (exponentials); with
+// d 128: 435 us (1.26 PFLOP/s) in short bursts, 501 us at the power cap; d 64 368 us (exponentials); with
 // capped scores 830 us. Short documents pay a near tile and 2.5k clocks of output a unit: 6151 tokens in
 // 24 documents 59 us. One issuing warp, not one per tile: with two, both tiles' products interleave and
 // both finish late (475 -> 537 us). Pairs always: a tile alone takes 0.83 of a pair's step, so units of
@@ -475,25 +475,29 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                 if (grow) m_ref = mt;
                 const float neg = (m_ref == -INFINITY) ? 0.f : -m_ref * C;
                 const uint64_t c2 = pk2(C, C), n2 = pk2(neg, neg);
-                uint64_t sum = 0ull;
+                uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
+                    // in passes over the chunk: independent instructions stand next to each other (d 64: 375 -> 368 us)
                     uint32_t w[16];
 #pragma unroll
+                    for (int e = 0; e < 32; e += 2) upk2(fma2(pk2(x[c + e], x[c + e + 1]), c2, n2), x[c + e], x[c + e + 1]);
+#pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float a, b;
-                        upk2(fma2(pk2(x[c + e], x[c + e + 1]), c2, n2), a, b);
                         // a quarter of the exponentials on the FMA pipe, where exponentials bound the kernel (d 64: 388 ->
                         // 371 us, with a cap 874 -> 842); at d 128 the products and the power cap hold it and that costs
                         // or changes nothing (454 -> 466 us, with a cap 823 -> 825; 8192 tokens, 32/8 heads)
                         if (D == 64 && e % 8 == 6) {
-                            exp2_poly2<4>(a, b);
+                            exp2_poly2<4>(x[c + e], x[c + e + 1]);
                         } else {
-                            a = ex2_approx(a);
-                            b = ex2_approx(b);
+                            x[c + e] = ex2_approx(x[c + e]);
+                            x[c + e + 1] = ex2_approx(x[c + e + 1]);
                         }
-                        sum = add2(sum, pk2(a, b));
-                        w[e / 2] = pack_bf16(a, b);   // weights enter P V as bf16: 2^-9 each, as the output's own rounding
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        sums[(e / 2) & 3] = add2(sums[(e / 2) & 3], pk2(x[c + e], x[c + e + 1]));
+                        w[e / 2] = pack_bf16(x[c + e], x[c + e + 1]);   // weights enter P V as bf16: 2^-8 each, as the output's own rounding
                     }
                     tmem_st16(ts + c / 2, w);
                     if (c == 32) {
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                     }
                 }
                 float s0, s1;
-                upk2(sum, s0, s1);
+                upk2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), s0, s1);
                 l_sum += s0 + s1;
                 tmem_st_wait();
                 tc_fence_before();
