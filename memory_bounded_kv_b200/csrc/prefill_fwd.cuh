@@ -28,7 +28,7 @@
 // and takes some 3400, the rest being the hand-over between products and softmax: a tile's next S waits
 // for its P V, because two S and two O fill the tensor memory. One document of 8192 tokens, 32/8 heads,
 // d 128: 435 us (1.26 PFLOP/s) in short bursts, 501 us at the power cap; d 64 368 us (exponentials); with
-// capped scores 830 us. Short documents pay a near tile and 2.5k clocks of output a unit: 6151 tokens in
+// capped scores 800 us. Short documents pay a near tile and 2.5k clocks of output a unit: 6151 tokens in
 // 24 documents 59 us. One issuing warp, not one per tile: with two, both tiles' products interleave and
 // both finish late (475 -> 537 us). Pairs always: a tile alone takes 0.83 of a pair's step, so units of
 // one tile lose even where the longest pair holds up the rest (4000 tokens in 5 documents, 16/2 heads, d 64,
@@ -414,11 +414,96 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
             step += n - nt;
             if (nt == 0) continue;
             float m_ref = -INFINITY, l_sum = 0.f;
+            // 32 scores to their weights (bf16, into tensor memory at dst) and into the sums
+            auto weights = [&](float* x, uint64_t c2, uint64_t n2, uint64_t (&sums)[4], uint32_t dst) {
+                // in passes, so that independent instructions stand next to each other (d 64: 375 -> 368 us)
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) upk2(fma2(pk2(x[e], x[e + 1]), c2, n2), x[e], x[e + 1]);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    // a quarter of the exponentials on the FMA pipe, where exponentials bound the kernel (d 64: 388 ->
+                    // 371 us, with a cap 874 -> 842); at d 128 the products and the power cap hold it and that costs
+                    // or changes nothing (454 -> 466 us, with a cap 823 -> 825; 8192 tokens, 32/8 heads)
+                    if (D == 64 && e % 8 == 6) {
+                        exp2_poly2<4>(x[e], x[e + 1]);
+                    } else {
+                        x[e] = ex2_approx(x[e]);
+                        x[e + 1] = ex2_approx(x[e + 1]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    sums[(e / 2) & 3] = add2(sums[(e / 2) & 3], pk2(x[e], x[e + 1]));
+                    w[e / 2] = pack_bf16(x[e], x[e + 1]);   // weights enter P V as bf16: 2^-8 each, as the output's own rounding
+                }
+                tmem_st16(dst, w);
+            };
+            // the first half's product starts while the second half is computed
+            auto half_done = [&] {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_half[t]);
+            };
+            auto all_done = [&](const uint64_t (&sums)[4]) {
+                float s0, s1;
+                upk2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), s0, s1);
+                l_sum += s0 + s1;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
+            };
             for (int tile = nt - 1; tile >= 0; --tile, ++step, ++sc) {
                 if (!warp_wait(&s_full[t], (unsigned)sc & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
                 const int j0 = tile * KT, st = step % ST;
                 const bool biased = BETA && (CAP || j0 + KT > first + 1), masked = j0 + KT > max(first + 1, pre);
+                if (CAP && !masked && tile < nt - 1) {
+                    // No score passes the uncapped one's size or the cap, and no bias of a log beta <= 0 raises it: where
+                    // that bound stays within 2^16 of the reference, the reference stays, and the tile needs one pass
+                    // and no write of the capped scores (8192 tokens, cap 50, d 128: 811 -> 759 us)
+                    bool low = true;                             // (not where a log beta is NaN)
+                    const float* lbf = reinterpret_cast<const float*>(smem + SH::LB_OFF) + st * KT;
+                    if (biased) {
+                        if (!warp_wait(&lb_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
+#pragma unroll
+                        for (int e = 0; e < 128; e += 32) low = low && lbf[lane + e] <= 0.f;
+                    }
+                    float x[128];
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) tmem_ld32(ts + c, x + c);
+                    tmem_ld_wait();
+                    float mx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 128; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], fabsf(x[c + 2 * e]), fabsf(x[c + 2 * e + 1]));
+                    const float most = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    if (__all_sync(kFull, low && fminf(most * p.scale * kLog2e, cap2) - m_ref <= 16.f)) {
+                        const bool tiny = cap_tiny(most, per_cap), small = cap_small(most, per_cap);
+                        const uint64_t c2 = pk2(C, C), n2 = pk2(-m_ref, -m_ref);
+                        uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 32) {
+                            float y[32];
+                            tmem_ld32(ts + c, y);
+                            tmem_ld_wait();
+                            if (tiny)
+                                cap_by_2(y, per_cap, cap2);
+                            else if (small)
+                                cap_by_4(y, per_cap, cap2);
+                            else
+                                cap_by_exp(y, per_cap, cap2);
+                            if (biased) add_bias(y, reinterpret_cast<const float4*>(lbf + c), (float)(i - j0 - c), j0 + KT <= first + 1);
+                            weights(y, c2, n2, sums, ts + c / 2);
+                            if (c == 32) half_done();
+                        }
+                        all_done(sums);
+                        continue;
+                    }
+                }
                 if (CAP || biased || masked) {
                     // the cap, the bias and the mask of these tiles go into S itself
                     if (biased && !warp_wait(&lb_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
@@ -478,43 +563,10 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                 uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
-                    // in passes over the chunk: independent instructions stand next to each other (d 64: 375 -> 368 us)
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) upk2(fma2(pk2(x[c + e], x[c + e + 1]), c2, n2), x[c + e], x[c + e + 1]);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        // a quarter of the exponentials on the FMA pipe, where exponentials bound the kernel (d 64: 388 ->
-                        // 371 us, with a cap 874 -> 842); at d 128 the products and the power cap hold it and that costs
-                        // or changes nothing (454 -> 466 us, with a cap 823 -> 825; 8192 tokens, 32/8 heads)
-                        if (D == 64 && e % 8 == 6) {
-                            exp2_poly2<4>(x[c + e], x[c + e + 1]);
-                        } else {
-                            x[c + e] = ex2_approx(x[c + e]);
-                            x[c + e + 1] = ex2_approx(x[c + e + 1]);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        sums[(e / 2) & 3] = add2(sums[(e / 2) & 3], pk2(x[c + e], x[c + e + 1]));
-                        w[e / 2] = pack_bf16(x[c + e], x[c + e + 1]);   // weights enter P V as bf16: 2^-8 each, as the output's own rounding
-                    }
-                    tmem_st16(ts + c / 2, w);
-                    if (c == 32) {
-                        // the first half's product starts while the second half is computed
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_half[t]);
-                    }
+                    weights(x + c, c2, n2, sums, ts + c / 2);
+                    if (c == 32) half_done();
                 }
-                float s0, s1;
-                upk2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), s0, s1);
-                l_sum += s0 + s1;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
+                all_done(sums);
             }
             if (stop) break;
             if (!warp_wait(&o_full[t], (unsigned)oc & 1u, p.wait_ns)) { stop = true; break; }

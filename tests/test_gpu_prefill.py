@@ -236,6 +236,34 @@ def test_large_scores():
     np.testing.assert_allclose(f64(lse), r["lse"], rtol=2e-6, atol=1e-4)
 
 
+@pytest.mark.parametrize("climb", ["scores", "log_beta", "nan"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (2, 1, 128)])
+def test_capped_scores_that_climb_with_the_distance(climb, Hq, Hkv, d):
+    """Far keys weigh more than near ones by far more than a tile's reference leaves room for.
+
+    lse: scores of +-60 are off by 2^-22 of 64, a cap of 40 by 2^-21 of it: 1.5e-5 + 1.9e-5."""
+    cu, T, cap = [0, 700, 900], 901, 40.0
+    c = make(30, cu, T, Hq, Hkv, d)
+    if climb == "scores":
+        c["q"] = (c["q"] * 0.05 + 1).to(torch.bfloat16)
+        sign = torch.where(torch.arange(T) < 300, 1.0, -1.0).cuda()[:, None, None]
+        c["k"] = (c["k"] * 0.05 + sign * 60 / d ** 0.5).to(torch.bfloat16)
+        c["lb"] = c["lb"] * 1e-3
+    else:
+        c["lb"][:300] = 0.05                 # up to 35 at 700 tokens
+    r = reference(c, None, cap)
+    if climb == "nan":
+        c["lb"][700:] = float("nan")         # the second document's own
+        c["lb"][900:] = -1.0
+        o, lse = forward(c, None, cap)
+        assert rel(f64(o)[:700], r["o"][:700]) <= REL
+        assert torch.isnan(lse[701:900]).all()
+    else:
+        o, lse = forward(c, None, cap)
+        check(o, r["o"], REL, climb)
+    np.testing.assert_allclose(f64(lse)[:700], r["lse"][:700], rtol=2e-6, atol=4e-5)
+
+
 def test_other_documents_and_padding_do_not_leak():
     """NaN and infinities in a neighbour document's rows, and behind the last one, reach nobody else."""
     T, Hq, Hkv, d = 310, 8, 2, 128
