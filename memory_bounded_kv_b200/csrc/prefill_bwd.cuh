@@ -428,8 +428,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 if (lane == 0) mbar_arrive(s_read);
                 const bool past = (tile + 1) * KT <= first + 1;
                 if (CAP) {
-                    cap_scores(x, per_cap, cap2);
-                    cap_scores(x + 32, per_cap, cap2);
+                    cap_scores<64>(x, per_cap, cap2);
 #pragma unroll
                     for (int c = 0; c < 64; ++c) th[c] = x[c];
                 }
@@ -457,7 +456,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     x[c] = u;
                     x[c + 1] = v;
                 }
-                uint64_t sum = 0ull;
+                uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
                 if (!warp_wait(dp_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
                 if (n == 1) {
@@ -493,7 +492,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const uint64_t ds = mul2(pk2(x[c0 + e], x[c0 + e + 1]), add2(pk2(dp[e], dp[e + 1]), e2));
-                        sum = add2(sum, ds);
+                        sums[(e / 2) & 3] = add2(sums[(e / 2) & 3], ds);
                         float u, v;
                         upk2(CAP ? mul2(ds, cap_slope2(th[c0 + e], th[c0 + e + 1], inv_cap2)) : ds, u, v);
                         w[e / 2] = pack_bf16(u, v);   // dS enters dS K as bf16: 2^-8 each, as dq's own rounding
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     tmem_st16(tl + SH::TM_DP + t * 64 + c0 / 2, w);
                 }
                 float s0, s1;
-                upk2(sum, s0, s1);
+                upk2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), s0, s1);
                 rsum += s0 + s1;
                 tmem_st_wait();
                 tc_fence_before();
@@ -979,8 +978,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 if (CAP) {
                     if (!warp_wait(&x_full[st], (unsigned)(step / ST) & 1u, p.wait_ns)) { stop = true; break; }
                     const float4* l4 = reinterpret_cast<const float4*>(smem + SH::ROW_OFF + (st * QT + 64 * t) * 4);
-                    cap_scores(x, per_cap, cap2);
-                    cap_scores(x + 32, per_cap, cap2);
+                    cap_scores<64>(x, per_cap, cap2);
                     // + (di + c >> lg) b where all is past: by blocks of eight columns
                     const float in_block = BETA && past ? slope_b : 0.f, per_block = in_block * (float)(8 >> lg);
                     uint64_t by2[4];

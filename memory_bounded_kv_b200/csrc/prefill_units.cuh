@@ -323,52 +323,58 @@ __device__ __forceinline__ void store_bf16x32(void* dst, const float (&o)[32], f
 // tanh(y) = 1 - 2 / (1 + e^2y): off by about 2^-23 absolute
 __device__ __forceinline__ float tanh_exp(float y) { return 1.f - 2.f * rcp_approx(1.f + ex2_approx(2.f * kLog2e * y)); }
 
-// x = amp tanh(per_cap x), 32 values: where a warp's y = per_cap x are small (scores small beside the cap, the
+// x = amp tanh(per_cap x), N values: where a warp's y = per_cap x are small (scores small beside the cap, the
 // common case) by y times the polynomial in y^2 whose largest relative error is smallest, which also keeps
 // small values to fp32 accuracy: degree 2 for y^2 <= 1/32 (5e-8; scores of variance 1 beside a cap of 25), with
-// per_cap in the coefficients, degree 4 for y^2 <= 1/4 (1.3e-8); else through the exponential. `most` is the largest |x| of each thread.
+// per_cap in the coefficients, degree 4 for y^2 <= 1/4 (1.3e-8); else through the exponential.
+// `most` is the largest |x| of each thread. One choice for 64 values beats two for 32 in the gradients (8192
+// tokens, cap 50, d 128: 1137 -> 1090 and 1291 -> 1240 us).
 __device__ __forceinline__ bool cap_tiny(float most, float per_cap) {
     // the coefficients' range: per_cap^4 and x^2 stay normal numbers
     return __all_sync(kFull, most * per_cap <= 0.17677669f) && per_cap >= 1e-6f && per_cap <= 1e6f;
 }
 __device__ __forceinline__ bool cap_small(float most, float per_cap) { return __all_sync(kFull, most * per_cap <= 0.5f); }
 
+template <int N = 32>
 __device__ __forceinline__ void cap_by_2(float* x, float per_cap, float amp) {
     const float k1 = amp * per_cap, k2 = per_cap * per_cap;
     const uint64_t c2 = same2(k1 * k2 * k2 * 0.13083961606025696f), c1 = same2(k1 * k2 * -0.333304226398468f), c0 = same2(k1);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
+    for (int c = 0; c < N; c += 2) {
         const uint64_t z = pk2(x[c], x[c + 1]), u = mul2(z, z);
         upk2(mul2(fma2(fma2(c2, u, c1), u, c0), z), x[c], x[c + 1]);
     }
 }
 
+template <int N = 32>
 __device__ __forceinline__ void cap_by_4(float* x, float per_cap, float amp) {
     const uint64_t c4 = same2(amp * 0.017135005444288254f), c3 = same2(amp * -0.05298607423901558f),
                    c2 = same2(amp * 0.13324779272079468f), c1 = same2(amp * -0.3333306908607483f), c0 = same2(amp);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
+    for (int c = 0; c < N; c += 2) {
         const uint64_t y = mul2(pk2(x[c], x[c + 1]), same2(per_cap)), u = mul2(y, y);
         const uint64_t r = fma2(fma2(fma2(fma2(c4, u, c3), u, c2), u, c1), u, c0);
         upk2(mul2(r, y), x[c], x[c + 1]);
     }
 }
 
+template <int N = 32>
 __device__ __forceinline__ void cap_by_exp(float* x, float per_cap, float amp) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) x[c] = amp * tanh_exp(x[c] * per_cap);
+    for (int c = 0; c < N; ++c) x[c] = amp * tanh_exp(x[c] * per_cap);
 }
 
+template <int N = 32>
 __device__ __forceinline__ void cap_scores(float* x, float per_cap, float amp) {
     float most = 0.f;
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) most = max3(most, fabsf(x[c]), fabsf(x[c + 1]));
+    for (int c = 0; c < N; c += 2) most = max3(most, fabsf(x[c]), fabsf(x[c + 1]));
     if (cap_tiny(most, per_cap))
-        cap_by_2(x, per_cap, amp);
+        cap_by_2<N>(x, per_cap, amp);
     else if (cap_small(most, per_cap))
-        cap_by_4(x, per_cap, amp);
+        cap_by_4<N>(x, per_cap, amp);
     else
-        cap_by_exp(x, per_cap, amp);
+        cap_by_exp<N>(x, per_cap, amp);
 }
 
 // the derivative 1 - tanh^2 of a pair of capped scores x = amp tanh(.); minus_inv = -1 / amp^2
