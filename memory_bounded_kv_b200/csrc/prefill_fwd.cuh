@@ -258,13 +258,19 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                 for (int q = q0; q < n; q += 2) {
                     const int tile = n - 1 - q, k = step + q, st = k % ST;
                     const unsigned ph = (unsigned)(k / ST) & 1u;
+                    const bool tail = (tile + 1) * KT > len;   // a document's last tile: the unit's first step
+                    float b[4];
                     if (BETA) {
-                        float b[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) b[e] = clamp_log_beta(nb[e]) * unit_b;
                         load(tile - 2);
-                        // the slopes of step k - ST were read before its P V product, which freed the V stage
-                        if (k >= ST && !warp_wait(&v_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
+                    }
+                    // The V stage is free: the slopes of step k - ST were read before the P V product that freed it,
+                    // and its V had landed. (Without that v_full could be a phase behind, and the wait on it below
+                    // would pass at once. No barrier can be ahead: the step's products wait for its slopes or for its
+                    // clearing, and steps with neither do not wait here.)
+                    if ((BETA || tail) && k >= ST && !warp_wait(&v_empty[st], ph ^ 1u, p.wait_ns)) { stop = true; break; }
+                    if (BETA) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             reinterpret_cast<float*>(smem + SH::LB_OFF)[st * KT + lane + 32 * e] = b[e];
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                             if (lane == 0) mbar_arrive(&k_full[st]);
                         }
                     }
-                    if ((tile + 1) * KT > len) {
+                    if (tail) {
                         if (!warp_wait(&v_full[st], ph, p.wait_ns)) { stop = true; break; }
                         const int rows = len - tile * KT;
                         unsigned char* vt = smem + SH::V_OFF + st * SH::TILE;

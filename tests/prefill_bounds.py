@@ -1,0 +1,57 @@
+"""Bounds, value by value, on what the prompt-path kernels may be off by, in float64 on the host (numpy).
+
+A rounding to bf16 is off by at most 2^-8 of the value. ETA is what a softmax weight may be off by,
+relative to itself, before that rounding: 4e-6 from its logit (an fp32 sum of d products whose partial
+sums stay below 16), as much from the row's lse or sum, 2.6e-6 from the exponential: below 2^-16."""
+import numpy as np
+
+BF16, ETA = 2.0 ** -8, 2.0 ** -16
+SLACK = 1.01   # products of two of the errors
+
+
+def pairs(q, k, log_beta, g, h, s, e, pre, softcap, scale):
+    """(p, slope, age) of a document's rows s .. e, query head h of kv head g."""
+    i, j = np.arange(e - s)[:, None], np.arange(e - s)[None, :]
+    x = scale * (q[s:e, h].astype(np.float64) @ k[s:e, g].astype(np.float64).T)
+    slope = np.ones_like(x)
+    if softcap:
+        t = np.tanh(x / softcap)
+        x, slope = softcap * t, 1 - t * t
+    age = np.maximum(i - j, 0).astype(np.float64)
+    if log_beta is not None:
+        x = x + age * log_beta[s:e, g].astype(np.float64)[None, :]
+    x = np.where(j < np.maximum(i + 1, pre), x, -np.inf)
+    p = np.exp(x - x.max(1, keepdims=True))
+    return p / p.sum(1, keepdims=True), slope, age
+
+
+def documents(cu, prefix):
+    for n in range(len(cu) - 1):
+        s, e = int(cu[n]), int(cu[n + 1])
+        if e > s:
+            yield s, e, 0 if prefix is None else min(max(int(prefix[n]), 0), e - s)
+
+
+def forward(q, k, v, log_beta, cu, prefix=None, softcap=0.0, scale=0.0):
+    """o and the bound on its error, [T, Hq, d]; rows of no document are NaN. The weights enter P V as bf16
+    (BF16 of p |v| for each key), their sum does not, and o is rounded once."""
+    T, Hq, d = q.shape
+    G = Hq // k.shape[1]
+    o, bound = np.full((T, Hq, d), np.nan), np.full((T, Hq, d), np.nan)
+    for s, e, pre in documents(cu, prefix):
+        for h in range(Hq):
+            g = h // G
+            p, _, _ = pairs(q, k, log_beta, g, h, s, e, pre, softcap, scale or d ** -0.5)
+            vv = v[s:e, g].astype(np.float64)
+            o[s:e, h] = p @ vv
+            bound[s:e, h] = SLACK * (BF16 * np.abs(o[s:e, h]) + (BF16 + 2 * ETA) * (p @ np.abs(vv)))
+    return o, bound
+
+
+def within(got, want, bound, what):
+    """Every value of the documents' rows within its bound."""
+    rows = ~np.isnan(want.reshape(want.shape[0], -1)[:, 0])
+    off = np.abs(got[rows] - want[rows]) - bound[rows]
+    bad = ~(off <= 0)
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} values out of bounds, the first at "
+                           f"{tuple(int(x[0]) for x in np.nonzero(bad))} of the documents' rows, by {off[bad].max():.3e}")
