@@ -257,14 +257,22 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 
 __device__ __forceinline__ uint64_t same2(float a) { return pk2(a, a); }
 
-// 2^x of a pair on the FMA pipe, for x <= 128 (below -126 as at -126): with n the nearest integer (left
-// in the low bits of x + 1.5 2^23) and f = x - n in [-1/2, 1/2], 2^f by the polynomial of degree DEG whose
+// the larger of two, NaN where one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 2^x of a pair on the FMA pipe, for x < 128; 0 below -126.5 (-inf too), NaN stays. With n the nearest integer
+// (left in the low bits of x + 1.5 2^23) and f = x - n in [-1/2, 1/2], 2^f by the polynomial of degree DEG whose
 // largest relative error is smallest (4: 2.6e-6, 5: 7.5e-8; found by a weighted least-squares iteration),
-// times 2^n by an addition to the exponent.
+// times 2^n. That is a product and not an addition to the exponent's bits: those of NaN would come out finite,
+// and n = -127, where the lower bound of x ends, gives the factor 0.
 template <int DEG>
 __device__ __forceinline__ void exp2_poly2(float& a, float& b) {
     static_assert(DEG == 4 || DEG == 5, "degree");
-    const uint64_t x = pk2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+    const uint64_t x = pk2(max_nan(a, -127.f), max_nan(b, -127.f));
     const uint64_t t = add2(x, same2(12582912.f));
     const uint64_t f = fma2(add2(t, same2(-12582912.f)), same2(-1.f), x);
     uint64_t r;
@@ -281,10 +289,9 @@ __device__ __forceinline__ void exp2_poly2(float& a, float& b) {
         r = fma2(r, f, same2(1.0000001192092896f));
     }
     float ta, tb;
-    upk2(r, a, b);
     upk2(t, ta, tb);
-    a = __uint_as_float(__float_as_uint(a) + (__float_as_uint(ta) << 23));
-    b = __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23));
+    upk2(mul2(r, pk2(__uint_as_float((__float_as_uint(ta) << 23) + 0x3f800000u),
+                     __uint_as_float((__float_as_uint(tb) << 23) + 0x3f800000u))), a, b);
 }
 
 // the larger of three (NaN is passed over, as fmaxf does)
