@@ -428,6 +428,10 @@ kvb_status kvb_paged_compact_blocks(const kvb_paged_cache* cache, const int32_t*
  * Rows of no document are neither read into a result nor written. A document
  * may be empty. cu out of order or outside [0, T] sets KVB_DERR_RANGE and
  * nothing is written.
+ * A CTA whose bounded wait runs out sets KVB_DERR_TIMEOUT and gives up: the
+ * rows of the results that it had not written keep what they held, and so do
+ * the rows of dk, dv and d_log_beta whose sum it holds a part of -- all their
+ * rows where a CTA of the gradients by query rows gave up (delta is missing).
  * An infinity or a NaN in a row reaches no other document. One in v_j or d_o_i
  * may also reach pairs (i, j) of the same document that do not see each other
  * (their weight is 0, and 0 times it is NaN), as in the formula's products.
@@ -724,6 +728,15 @@ int32_t kvb_abi_version(void);
  * KVB_EINVAL. Not for production use.
  * ---------------------------------------------------------------------- */
 kvb_status kvb_test_withhold_next_decode(uint64_t wait_limit_ns);
+
+/* kvb_test_withhold_next_prefill: the next kvb_prefill_attn (kernel 0) or
+ * kvb_prefill_attn_bwd (kernel 1: by query rows, 2: by keys) call in this
+ * process launches that kernel with one CTA (0 .. 65535) whose loads end after
+ * its first tile; the waits of its other roles run out after wait_limit_ns
+ * nanoseconds (1000 .. 1e9, else KVB_EINVAL) and the CTA gives up: see the
+ * two calls for what it leaves. A CTA that the kernel does not have, or that
+ * has one tile to load, changes nothing. Not for production use. */
+kvb_status kvb_test_withhold_next_prefill(int32_t kernel, int32_t cta, uint64_t wait_limit_ns);
 
 #ifdef __cplusplus
 }

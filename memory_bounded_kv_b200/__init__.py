@@ -30,6 +30,7 @@ __all__ = [
     "kvb_asm_entries_bf16", "kvb_asm_index_workspace_bytes", "kvb_asm_index_csr",
     "kvb_asm_lookup_merge_grouped", "kvb_asm_aggregate_grouped",
     "kvb_get_error", "kvb_abi_version", "kvb_test_withhold_next_decode",
+    "kvb_test_withhold_next_prefill",
     "decode_workspace", "evict_candidates",
     "PagedPool", "kvb_paged_reset", "kvb_paged_evict_insert", "kvb_paged_decode_attn", "kvb_paged_compact_blocks",
     "kvb_asm_planes_bytes", "kvb_asm_prepare", "kvb_asm_lookup_merge_planes",
@@ -119,6 +120,13 @@ def kvb_test_withhold_next_decode(wait_limit_ns: int) -> None:
     """Testing hook: the next decode-attention call's producers withhold their copies, so its
     bounded waits run out after wait_limit_ns (see kvb_test_withhold_next_decode in kvb.h)."""
     _check(_lib.lib().kvb_test_withhold_next_decode(int(wait_limit_ns)), "kvb_test_withhold_next_decode")
+
+
+def kvb_test_withhold_next_prefill(kernel: int, cta: int, wait_limit_ns: int) -> None:
+    """Testing hook: one CTA of the next prompt-attention kernel (0: forward, 1: gradients by query
+    rows, 2: by keys) loads its first tile alone, so its bounded waits run out after wait_limit_ns."""
+    _check(_lib.lib().kvb_test_withhold_next_prefill(int(kernel), int(cta), int(wait_limit_ns)),
+           "kvb_test_withhold_next_prefill")
 
 
 def kvb_get_error(stream=None) -> int:

@@ -20,7 +20,7 @@ EXPORTS = (
     "kvb_asm_entries_bf16", "kvb_asm_index_workspace_bytes", "kvb_asm_index_csr",
     "kvb_asm_lookup_merge_grouped", "kvb_asm_aggregate_grouped",
     "kvb_get_error", "kvb_status_str",
-    "kvb_abi_version", "kvb_test_withhold_next_decode",
+    "kvb_abi_version", "kvb_test_withhold_next_decode", "kvb_test_withhold_next_prefill",
     "kvb_paged_reset", "kvb_paged_evict_insert", "kvb_paged_decode_attn", "kvb_paged_compact_blocks",
     "kvb_asm_planes_bytes", "kvb_asm_prepare", "kvb_asm_lookup_merge_planes",
     "kvb_prefill_attn", "kvb_prefill_attn_bwd_workspace_bytes", "kvb_prefill_attn_bwd",
@@ -128,6 +128,7 @@ def lib() -> ctypes.CDLL:
         L.kvb_status_str.restype = ctypes.c_char_p
         L.kvb_abi_version.argtypes = []
         L.kvb_test_withhold_next_decode.argtypes = [ctypes.c_uint64]
+        L.kvb_test_withhold_next_prefill.argtypes = [_I32, _I32, ctypes.c_uint64]
         _PC = ctypes.POINTER(PagedCacheArgs)
         L.kvb_paged_reset.argtypes = [_PC, _P]
         L.kvb_paged_evict_insert.argtypes = [_PC, _P, _P, _P, _P, _I32, _P, _P, _I32, _P]
@@ -151,7 +152,7 @@ def lib() -> ctypes.CDLL:
                   "kvb_asm_lookup_merge", "kvb_asm_hier_lookup_merge", "kvb_asm_aggregate",
                   "kvb_asm_entries_bf16", "kvb_asm_index_csr", "kvb_asm_lookup_merge_grouped",
                   "kvb_asm_aggregate_grouped", "kvb_get_error",
-                  "kvb_abi_version", "kvb_test_withhold_next_decode", "kvb_paged_reset",
+                  "kvb_abi_version", "kvb_test_withhold_next_decode", "kvb_test_withhold_next_prefill", "kvb_paged_reset",
                   "kvb_paged_evict_insert", "kvb_paged_decode_attn", "kvb_paged_compact_blocks",
                   "kvb_asm_prepare", "kvb_asm_lookup_merge_planes", "kvb_prefill_attn",
                   "kvb_prefill_attn_bwd", "kvb_paged_plan", "kvb_paged_write"):

@@ -2,6 +2,7 @@
 // gradients, page planning and page writes. As in kvb.cu, the host code validates, picks the
 // kernel and launches it on the caller's stream; it allocates nothing.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "host.cuh"
@@ -15,6 +16,18 @@ namespace {
 
 inline size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Test hook of kvb_test_withhold_next_prefill: wait limit (ns) | kernel << 32 | (CTA + 1) << 40; 0 = off. Taken
+// (and cleared) by the next call that launches the kernel.
+std::atomic<unsigned long long> g_withhold_prefill{0};
+
+bool take_withheld(unsigned kernel, kvb::PrefillParams* p) {
+    unsigned long long x = g_withhold_prefill.load(std::memory_order_relaxed);
+    if (x == 0 || ((x >> 32) & 255) != kernel || !g_withhold_prefill.compare_exchange_strong(x, 0)) return false;
+    p->wait_ns = x & 0xffffffffull;
+    p->withhold = (int)(x >> 40);
+    return true;
+}
 
 // The host checks of kvb_prefill_attn and its gradients, and the kernels' parameters.
 kvb_status prefill_params(const kvb_prefill_args* a, kvb::PrefillParams* out) {
@@ -94,7 +107,7 @@ kvb_status fwd_dispatch(const kvb::PrefillParams& p, cudaStream_t st) {
 }
 
 template <int D, bool BETA, bool CAP>
-kvb_status launch_bwd(const kvb::PrefillParams& p, cudaStream_t st) {
+kvb_status launch_bwd(kvb::PrefillParams p, cudaStream_t st) {
     using SQ = kvb::DqShape<D>;
     using SK = kvb::DkvShape<D>;
     auto kq = kvb::prefill_dq_kernel<D, BETA, CAP>;
@@ -106,8 +119,11 @@ kvb_status launch_bwd(const kvb::PrefillParams& p, cudaStream_t st) {
         return KVB_EINVAL;
     int slots = resident_ctas(kq, SQ::NT, SQ::SMEM);
     if (slots <= 0) return KVB_ECUDA;
-    int grid = (int)std::min<long long>(slots, most_units(p, unit_shift(p) - 1));
-    if (launch_pdl(kq, dim3(grid), dim3(SQ::NT), SQ::SMEM, st, p, mk, mv) != KVB_OK) return KVB_ECUDA;
+    int grid = (int)std::min<long long>(std::min(slots, kvb::kMaxPieces), most_units(p, unit_shift(p) - 1));
+    p.dq_ctas = grid;
+    kvb::PrefillParams hooked = p;
+    take_withheld(1, &hooked);
+    if (launch_pdl(kq, dim3(grid), dim3(SQ::NT), SQ::SMEM, st, hooked, mk, mv) != KVB_OK) return KVB_ECUDA;
     if (!make_rows_map(&mq, p.q, D, p.Hq, p.T, p.q_sh, p.q_st, p.G, SK::QT / p.G) ||
         !make_rows_map(&mo, p.d_o, D, p.Hq, p.T, D, (long long)p.Hq * D, p.G, SK::QT / p.G) ||
         !make_rows_map(&mk, p.k, D, p.Hkv, p.T, p.kv_sh, p.kv_st, 1, SK::KT) ||
@@ -116,7 +132,9 @@ kvb_status launch_bwd(const kvb::PrefillParams& p, cudaStream_t st) {
     slots = resident_ctas(kk, SK::NT, SK::SMEM);
     if (slots <= 0) return KVB_ECUDA;
     grid = std::min(slots, kvb::kMaxPieces);
-    if (launch_pdl(kk, dim3(grid), dim3(SK::NT), SK::SMEM, st, p, mq, mo, mk, mv) != KVB_OK) return KVB_ECUDA;
+    hooked = p;
+    take_withheld(2, &hooked);
+    if (launch_pdl(kk, dim3(grid), dim3(SK::NT), SK::SMEM, st, hooked, mq, mo, mk, mv) != KVB_OK) return KVB_ECUDA;
     return launch_pdl(kvb::prefill_dkv_sum_kernel<D, BETA>, dim3(grid, 2 * D / 16), dim3(256), 0, st, p);
 }
 
@@ -131,17 +149,24 @@ kvb_status bwd_dispatch(const kvb::PrefillParams& p, cudaStream_t st) {
 
 extern "C" {
 
+kvb_status kvb_test_withhold_next_prefill(int32_t kernel, int32_t cta, uint64_t wait_limit_ns) {
+    if (kernel < 0 || kernel > 2 || cta < 0 || cta > 65535 || wait_limit_ns < 1000ull || wait_limit_ns > 1000000000ull) return KVB_EINVAL;
+    g_withhold_prefill.store(wait_limit_ns | (unsigned long long)kernel << 32 | (unsigned long long)(cta + 1) << 40);
+    return KVB_OK;
+}
+
 kvb_status kvb_prefill_attn(const kvb_prefill_args* a, kvb_stream stream) {
     kvb::PrefillParams p;
     if (prefill_params(a, &p) != KVB_OK) return KVB_EINVAL;
     if (p.T == 0 || p.N == 0) return KVB_OK;
+    take_withheld(0, &p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return a->d == 128 ? fwd_dispatch<128>(p, st) : fwd_dispatch<64>(p, st);
 }
 
 size_t kvb_prefill_attn_bwd_workspace_bytes(int32_t T, int32_t Hq) {
     if (T < 1 || Hq < 1) return 0;
-    return round256((size_t)T * Hq * sizeof(float)) + (size_t)kvb::kMaxPieces * (2 * kvb::kPartFloats * sizeof(float) + sizeof(int4));
+    return round256((size_t)T * Hq * sizeof(float)) + (size_t)kvb::kMaxPieces * (2 * kvb::kPartFloats * sizeof(float) + sizeof(int4) + sizeof(int));
 }
 
 kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* a, const kvb_prefill_grads* g, kvb_stream stream) {
@@ -158,6 +183,7 @@ kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* a, const kvb_prefill_gra
     p.delta = static_cast<float*>(g->workspace);
     p.parts = p.delta + round256((size_t)a->T * a->Hq * sizeof(float)) / sizeof(float);
     p.records = reinterpret_cast<int4*>(p.parts + (size_t)kvb::kMaxPieces * 2 * kvb::kPartFloats);
+    p.dq_done = reinterpret_cast<int*>(p.records + kvb::kMaxPieces);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return a->d == 128 ? bwd_dispatch<128>(p, st) : bwd_dispatch<64>(p, st);
 }

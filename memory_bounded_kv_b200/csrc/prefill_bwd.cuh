@@ -198,8 +198,11 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 }
                 __syncwarp();
                 if (end) break;
+                bool withheld = false;
                 for (int tile = n - 1; tile >= 0; --tile, ++step) {
                     const int st = step % ST;
+                    withheld = step > 0 && p.withhold == blockIdx.x + 1;
+                    if (withheld) break;
                     if (step >= ST && !warp_wait(&kv_empty[st], (unsigned)((step / ST) - 1) & 1u, p.wait_ns)) { stop = true; break; }
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&kv_full[st], (unsigned)(2 * SH::KTILE));
@@ -212,6 +215,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     }
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
+                if (withheld) break;
             }
             if (stop && lane == 0) fail();
         } else if (warp == 10) {
@@ -540,12 +544,13 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
     if (warp == 8) {
         if (elect_one()) umma_commit(fin);   // by the lane that issued the products
         __syncwarp();
-        mbar_wait(fin, 0u, p.wait_ns);
+        mbar_wait(fin, 0u);
     }
     if (tid == 0 && *s_abort) {
         for (int k = max(0, s_steps[0] - ST); k < s_steps[0]; ++k)
             mbar_wait(&kv_full[k % ST], (unsigned)(k / ST) & 1u, 100000000ull);
     }
+    if (tid == 0) p.dq_done[blockIdx.x] = *s_abort ? 0 : 1;
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
@@ -671,6 +676,10 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REG_REST));
         if (warp == 9) {
             // ======================= units and loads =======================
+            // where a CTA of the kernel by query rows gave up, its deltas are not there: nothing is done
+            bool lost = false;
+            for (int c = lane; c < p.dq_ctas; c += 32) lost |= p.dq_done[c] == 0;
+            lost = __any_sync(kFull, lost);
             const StepLine line(p);
             const bool cut = line.cut(gridDim.x);
             const long long piece = line.piece(gridDim.x), x1 = min((blockIdx.x + 1) * piece, line.steps);
@@ -683,7 +692,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                 bool end;
                 int s = 0, len = 0, g = 0, pre = 0, j0 = 0, b0 = 0, b1 = 0, part = 0;
                 if (cut) {
-                    end = x >= x1;
+                    end = lost || x >= x1;
                     if (!end) {
                         const StepLine::At u = line.find(x);
                         const long long till = min(u.end, x1);
@@ -698,7 +707,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     }
                 } else {
                     long long u = PrefillWalk::nth(round, blockIdx.x, gridDim.x);
-                    end = round * gridDim.x >= walk.units;
+                    end = lost || round * gridDim.x >= walk.units;
                     if (!end && u >= walk.units) {
                         end = true;   // a last round without this CTA
                     }
@@ -739,8 +748,11 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     }
                     s_steps[1] = uc + 1;
                 }
+                bool withheld = false;
                 for (int b = b0; b < b1; ++b, ++step) {
                     const int st = step % ST;
+                    withheld = step > 0 && p.withhold == blockIdx.x + 1;
+                    if (withheld) break;
                     if (step >= ST && !warp_wait(&q_empty[st], (unsigned)((step / ST) - 1) & 1u, p.wait_ns)) { stop = true; break; }
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&q_full[st], (unsigned)(2 * SH::TILE));
@@ -753,7 +765,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     }
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
-                if (stop) break;
+                if (stop || withheld) break;
             }
             if (lane == 0) p.records[blockIdx.x] = record;
             if (stop && lane == 0) fail();
@@ -1147,12 +1159,13 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
     if (warp == 8) {
         if (elect_one()) umma_commit(fin);   // by the lane that issued the products
         __syncwarp();
-        mbar_wait(fin, 0u, p.wait_ns);
+        mbar_wait(fin, 0u);
     }
     if (tid == 0 && *s_abort) {
         for (int k = max(0, s_steps[0] - ST); k < s_steps[0]; ++k)
             mbar_wait(&q_full[k % ST], (unsigned)(k / ST) & 1u, 100000000ull);
         if (s_steps[1] > 0) mbar_wait(k_full, (unsigned)(s_steps[1] - 1) & 1u, 100000000ull);
+        p.records[blockIdx.x].w = -2;
     }
     __syncthreads();
     if (warp == 8) {
@@ -1163,14 +1176,18 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
 
 // The key blocks that a cut goes through: the sums of their pieces, in order. blockIdx.x names the piece that
 // holds a key block's first step and not its last; a thread sums one key's 8 columns of dV or dK (the parts are
-// [column][key], so that a warp's accesses are whole lines).
+// [column][key], so that a warp's accesses are whole lines). A key block with a piece of a CTA that gave up stays
+// as it was.
 template <int D, bool BETA>
 __global__ void __launch_bounds__(256) prefill_dkv_sum_kernel(const __grid_constant__ PrefillParams p) {
     griddep_wait();
     griddep_launch_dependents();
     const int4 rec = p.records[blockIdx.x];
+    static_assert(kMaxPieces <= 256, "a thread per piece");
+    const int piece = threadIdx.x, state = piece < gridDim.x ? p.records[piece].w : -1;
+    if (rec.w < 0 || __syncthreads_or(piece > blockIdx.x && piece <= rec.w && state == -2)) return;
     const int r = threadIdx.x & 127;
-    if (rec.w < 0 || r >= rec.y) return;
+    if (r >= rec.y) return;
     const int col = (blockIdx.y * 2 + (threadIdx.x >> 7)) * 8;   // of dV's D columns, then dK's
     const float* first = p.parts + ((size_t)blockIdx.x * 2 + 1) * kPartFloats;
     const float* others = p.parts + (size_t)blockIdx.x * 2 * kPartFloats;   // + 2 q kPartFloats: the q-th piece after

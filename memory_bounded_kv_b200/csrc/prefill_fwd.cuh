@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                     break;
                 }
                 const int n = max(n0, n1);
+                bool withheld = false;
                 if (lane == 0) {
                     const int tiles = n1 > 0 ? 2 : 1;
                     mbar_arrive_expect_tx(q_full, (unsigned)(tiles * SH::TILE));
@@ -214,6 +215,8 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                 for (int tile = n - 1; tile >= 0; --tile, ++step) {
                     const int st = step % ST;
                     const unsigned ph = (unsigned)((step / ST) - 1) & 1u;
+                    withheld = step > 0 && p.withhold == blockIdx.x + 1;
+                    if (withheld) break;
                     if (step >= ST && !warp_wait(&k_empty[st], ph, p.wait_ns)) { stop = true; break; }
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&k_full[st], (unsigned)SH::TILE);
@@ -230,6 +233,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
                 if (stop && lane == 0) fail();
+                if (withheld) break;
             }
         } else if (warp >= 10) {
             // ======================= bias columns, V past a document's end =======================
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
         bool stop = false;
         for (int uc = 0; !stop; ++uc) {
             const int ub = uc & 1;
-            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) break;
+            if (!warp_wait(&u_full[ub], (unsigned)(uc >> 1) & 1u, p.wait_ns)) { stop = true; break; }
             const int* m = info + ub * 8;
             const int s = m[0], len = m[1], g = m[3], pre = m[4], n0 = m[5], n1 = m[6];
             const int first = m[2] + (t << (sh - 1));            // the tile's first token
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
     if (warp == 8) {
         if (elect_one()) umma_commit(fin);   // by the lane that issued the products
         __syncwarp();
-        mbar_wait(fin, 0u, p.wait_ns);
+        mbar_wait(fin, 0u);
     }
     if (tid == 0 && *s_abort) {
         for (int k = max(0, s_steps[0] - ST); k < s_steps[0]; ++k) {

@@ -18,6 +18,7 @@ struct PrefillParams {
     uint16_t* o;              // [T, Hq, d] bf16
     float* lse;               // [T, Hq] or null
     unsigned long long wait_ns;
+    int withhold;             // test hook: CTA withhold - 1 loads its first tile alone, so its other roles' waits run out (0: off)
     // gradients
     const uint16_t* d_o;      // [T, Hq, d]
     const float* d_lse;       // [T, Hq] or null
@@ -27,10 +28,13 @@ struct PrefillParams {
     uint16_t* dv;             // [T, Hkv, d]
     float* dlb;               // [T, Hkv] or null
     float* parts;             // [pieces][2] sums of key blocks that a cut goes through (kPartFloats each)
-    int4* records;            // [pieces] the key block that goes on behind a piece: first row, rows, kv head, last piece (-1: none)
+    int4* records;            // [pieces] the key block that goes on behind a piece: first row, rows, kv head, last piece
+                              // (-1: none; -2: the CTA gave up)
+    int* dq_done;             // [dq_ctas] whether a CTA of the kernel by query rows left all its deltas
+    int dq_ctas;
 };
 
-constexpr int kMaxPieces = 160;                          // CTAs of the kernel by keys, at most
+constexpr int kMaxPieces = 160;                          // CTAs of each gradient kernel, at most
 constexpr int kPartFloats = 2 * 128 * 128 + 128;         // dV^T, dK^T [d][128 keys], d log beta [128 keys]
 
 // A unit: block `blk` of 2^sh tokens of a document (rows s .. s + len) and a kv head.

@@ -48,6 +48,47 @@ def forward(q, k, v, log_beta, cu, prefix=None, softcap=0.0, scale=0.0):
     return o, bound
 
 
+def gradients(q, k, v, log_beta, cu, d_o, d_lse=None, prefix=None, softcap=0.0, scale=0.0):
+    """{name: (gradient, bound on its error)}; rows of no document are NaN. For each pair, with B = sum_c |d_o_c v_c|
+    and D its row's mean of B plus |d_lse|: dS = p (d_o.v - delta) is off by 2 ETA p (B + D) (p, the fp32 sums of
+    d_o.v and delta), P and dS enter the products as bf16, and dq, dk and dv are rounded once. dq of a row whose
+    tile of 128 / G tokens sees more than 128 keys takes delta from o as it was stored, whose error (`forward`'s
+    bound) meets |d_o| and then sum_j p k_j (times the cap's slope)."""
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    G = Hq // Hkv
+    scale = scale or d ** -0.5
+    _, o_bound = forward(q, k, v, log_beta, cu, prefix, softcap, scale)
+    shapes = dict(dq=(T, Hq, d), dk=(T, Hkv, d), dv=(T, Hkv, d), d_log_beta=(T, Hkv))
+    val, bnd = ({n: np.full(s, np.nan) for n, s in shapes.items()} for _ in range(2))
+    for s, e, pre in documents(cu, prefix):
+        first = np.arange(e - s) * G // 128 * 128 // G          # of each row's tile
+        far = np.maximum(np.minimum(first + 128 // G, e - s), pre) > 128
+        for x in (val, bnd):
+            for n in ("dk", "dv", "d_log_beta"):
+                x[n][s:e] = 0.0
+        for h in range(Hq):
+            g = h // G
+            p, slope, age = pairs(q, k, log_beta, g, h, s, e, pre, softcap, scale)
+            qq, kk, vv, do = (x.astype(np.float64) for x in (q[s:e, h], k[s:e, g], v[s:e, g], d_o[s:e, h]))
+            dl = np.zeros(e - s) if d_lse is None else d_lse[s:e, h].astype(np.float64)
+            dp = do @ vv.T
+            ds = p * (dp - ((p * dp).sum(1) - dl)[:, None])
+            b = np.abs(do) @ np.abs(vv).T
+            eds = 2 * ETA * p * (b + ((p * b).sum(1) + np.abs(dl))[:, None])
+            estimate = np.where(far, (np.abs(do) * o_bound[s:e, h]).sum(1), 0.0)
+            val["dq"][s:e, h] = scale * (ds * slope) @ kk
+            e16 = (eds + BF16 * np.abs(ds)) * slope             # dS as it enters the products
+            bnd["dq"][s:e, h] = scale * (e16 @ np.abs(kk) + estimate[:, None] * np.abs((p * slope) @ kk))
+            val["dk"][s:e, g] += scale * (ds * slope).T @ qq
+            bnd["dk"][s:e, g] += scale * e16.T @ np.abs(qq)
+            val["dv"][s:e, g] += p.T @ do
+            bnd["dv"][s:e, g] += (BF16 + 2 * ETA) * p.T @ np.abs(do)
+            val["d_log_beta"][s:e, g] += (ds * age).sum(0)
+            bnd["d_log_beta"][s:e, g] += (eds * age).sum(0)
+    return {n: (val[n], SLACK * (bnd[n] + (0.0 if n == "d_log_beta" else BF16 * np.abs(val[n])))) for n in shapes}
+
+
 def within(got, want, bound, what):
     """Every value of the documents' rows within its bound."""
     rows = ~np.isnan(want.reshape(want.shape[0], -1)[:, 0])
