@@ -392,7 +392,8 @@ kvb_status kvb_paged_compact_blocks(const kvb_paged_cache* cache, const int32_t*
  *
  *     s_ij   = scale * (q_i . k_j)
  *     x_ij   = cap(s_ij) + max(i - j, 0) * log_beta_j
- *     cap(s) = softcap * tanh(s / softcap)       (s when softcap == 0)
+ *     cap(s) = softcap * tanh(s / softcap)       (s when softcap == 0; the
+ *              decode calls have no cap)
  *     row i sees the keys j < max(i + 1, prefix_len[n]) of its document
  *     o_i    = sum_j softmax(x)_ij v_j,   lse_i = ln sum_j exp(x_ij)
  *

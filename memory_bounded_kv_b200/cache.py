@@ -166,10 +166,12 @@ class PagedKVCache:
         kvb_paged_compact_blocks(self.pool, rm_start, rm_len, stream=stream)
         self.cand_valid = False
 
-    def prefill(self, q, k, v, log_beta, cu, pos, o, lse=None, *, prefix_len=None, softcap=0.0, stream=None):
+    def prefill(self, q, k, v, log_beta, cu, pos, o, lse=None, *, prefix_len=None, stream=None):
         """Whole prompts at once: the packed tokens of sequence b (rows cu[b] .. cu[b + 1] of q
         [T, Hq, d], k, v [T, Hkv, d], log_beta [T, Hkv], pos [T]) attend among themselves
         (kvb_prefill_attn, into o and lse) and enter the cache (kvb_paged_plan, kvb_paged_write).
+        The attention is that of the decode steps (scores without a cap, scale 1/sqrt(d)) where pos
+        rises by one from token to token.
         A sequence with new tokens must hold none yet; one without keeps what it holds. The pages
         must have room for the whole prompts; the budget M is enforced by the insertions that
         follow, each of which replaces a slot of a sequence that holds M or more. kvb_get_error
@@ -194,7 +196,7 @@ class PagedKVCache:
             slot_map = torch.full((self.Hkv, k.shape[0]), -1, dtype=torch.int32, device=self.pool.len.device)
             workspace = torch.empty(kvb_paged_plan_workspace_bytes(self.B, self.Hkv), dtype=torch.uint8,
                                     device=self.pool.len.device)
-            kvb_prefill_attn(q, k, v, lb, cu, o, lse, prefix_len=prefix_len, softcap=softcap, stream=stream)
+            kvb_prefill_attn(q, k, v, lb, cu, o, lse, prefix_len=prefix_len, stream=stream)
             kvb_paged_plan(self.pool, cu, slot_map, workspace, empty_only=True, stream=stream)
             kvb_paged_write(self.pool, k, v, lb, pos, slot_map, stream=stream)
         self.cand_valid = False

@@ -1,8 +1,31 @@
 """Refusals of the prompt path that reach no device, beside those of test_prefill_host.py."""
 import pytest
+import torch
 
 import memory_bounded_kv_b200 as kvb
 from memory_bounded_kv_b200 import _lib
+from memory_bounded_kv_b200.cache import PagedKVCache
+from test_prefill_host import Hkv, Hq, N, T, args, d
+
+
+@pytest.fixture
+def cache(monkeypatch):
+    """A paged cache on the CPU whose kernels note that they were called, and arguments that it takes."""
+    monkeypatch.setattr(kvb, "kvb_paged_reset", lambda pool, stream=None: None)
+    c = PagedKVCache(N, Hq, Hkv, d, max_pages=2, num_pages=8, M=64, device="cpu")
+    c.called = []
+    for f in ("kvb_prefill_attn", "kvb_paged_plan", "kvb_paged_write"):
+        monkeypatch.setattr(kvb, f, lambda *a, _f=f, **k: c.called.append(_f))
+    a = args()
+    c.good = dict(q=a["q"], k=a["k"], v=a["v"], log_beta=a["log_beta"], cu=a["cu"], pos=torch.zeros(T, dtype=torch.int32), o=a["o"])
+    return c
+
+
+def test_cache_prefill_has_no_cap(cache):
+    """The decode steps that go on from a prompt have none, so a capped prompt would be another attention."""
+    with pytest.raises(TypeError):
+        cache.prefill(**cache.good, softcap=30.0)
+    assert cache.called == []
 
 
 @pytest.mark.parametrize("kernel,cta,limit", [(-1, 0, 10**6), (3, 0, 10**6), (0, -1, 10**6), (0, 65536, 10**6), (0, 0, 999),
