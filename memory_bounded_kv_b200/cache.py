@@ -185,6 +185,8 @@ class PagedKVCache:
             raise ValueError("cu must be [B + 1]")
         if tuple(pos.shape) != (T,) or pos.dtype != torch.int32 or not pos.is_contiguous():
             raise ValueError("pos must be [T] int32, contiguous")
+        if pos.device != k.device:
+            raise ValueError(f"pos is on {pos.device}, k on {k.device}")
         if (self.pool.log_beta_pages is not None) and log_beta is None:
             raise ValueError("log_beta is needed: the cache holds log betas")
         if stream is None:

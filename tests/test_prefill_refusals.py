@@ -28,6 +28,13 @@ def test_cache_prefill_has_no_cap(cache):
     assert cache.called == []
 
 
+def test_cache_prefill_refuses_positions_on_another_device(cache):
+    """Only the write reads them, and it comes after the plan has taken pages."""
+    with pytest.raises(ValueError, match="pos is on meta"):
+        cache.prefill(**dict(cache.good, pos=cache.good["pos"].to("meta")))
+    assert cache.called == []
+
+
 @pytest.mark.parametrize("kernel,cta,limit", [(-1, 0, 10**6), (3, 0, 10**6), (0, -1, 10**6), (0, 65536, 10**6), (0, 0, 999),
                                               (0, 0, 10**9 + 1)])
 def test_withholding_refuses(kernel, cta, limit):
