@@ -482,7 +482,8 @@ size_t kvb_prefill_attn_bwd_workspace_bytes(int32_t T, int32_t Hq);
 kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* args, const kvb_prefill_grads* grads, kvb_stream stream);
 
 /* ------------------------------------------------------------------------
- * kvb_paged_plan, kvb_paged_write -- whole prompts into a paged cache
+ * kvb_paged_plan, kvb_paged_plan_within, kvb_paged_write -- whole prompts into
+ * a paged cache
  *
  * kvb_paged_plan gives the tokens of packed prompts their slots: tokens
  * [cu[b], cu[b+1]) are appended to every kv head of sequence b. It takes
@@ -498,6 +499,9 @@ kvb_status kvb_prefill_attn_bwd(const kvb_prefill_args* args, const kvb_prefill_
  * KVB_DERR_PAGES is set. A sequence whose tokens do not fit its table, whose
  * len is out of range or, with empty_only != 0, that holds slots already while
  * it has new tokens, is not served either (KVB_DERR_LEN), and wants no pages.
+ * kvb_paged_plan_within does not serve (KVB_DERR_LEN) a sequence whose new
+ * tokens would make it hold more than max_len >= 1 slots: the insertions of a
+ * decode step keep a length above their budget, so that is where it is held.
  * A page outside the pool met on the way gives its tokens slot -1 and sets
  * KVB_DERR_RANGE.
  * slot_map entries of tokens outside all sequences are left as they were. cu
@@ -519,6 +523,10 @@ size_t kvb_paged_plan_workspace_bytes(int32_t B, int32_t Hkv);
 
 kvb_status kvb_paged_plan(const kvb_paged_cache* cache, const int32_t* cu, int32_t T, int32_t* slot_map,
                           int32_t empty_only, void* workspace, size_t workspace_bytes, kvb_stream stream);
+
+kvb_status kvb_paged_plan_within(const kvb_paged_cache* cache, const int32_t* cu, int32_t T, int32_t* slot_map,
+                                 int32_t empty_only, int32_t max_len, void* workspace, size_t workspace_bytes,
+                                 kvb_stream stream);
 
 kvb_status kvb_paged_write(const kvb_paged_cache* cache, const uint16_t* k, const uint16_t* v, int64_t kv_stride_t,
                            int64_t kv_stride_h, const float* log_beta, int64_t lb_stride_t, int64_t lb_stride_h,

@@ -831,12 +831,13 @@ def kvb_paged_plan_workspace_bytes(B: int, Hkv: int) -> int:
     return int(_lib.lib().kvb_paged_plan_workspace_bytes(B, Hkv))
 
 
-def kvb_paged_plan(pool, cu, slot_map, workspace, *, empty_only: bool = False, stream=None) -> None:
+def kvb_paged_plan(pool, cu, slot_map, workspace, *, empty_only: bool = False, max_len: int = 2**31 - 1,
+                   stream=None) -> None:
     """Pages and slots for the tokens of packed prompts; see kvb_paged_plan in include/kvb.h. cu
     [B + 1] int32: tokens cu[b] .. cu[b + 1] are appended to every kv head of sequence b; slot_map
     [Hkv, T] int32 receives the pool rows (-1: not served). workspace: a uint8 CUDA tensor of at
     least kvb_paged_plan_workspace_bytes(B, Hkv) bytes. empty_only: sequences that hold slots
-    already are not served."""
+    already are not served; max_len (kvb_paged_plan_within): nor are those that would hold more."""
     tensors = _pool_tensors(pool)
     _is(cu, _I32, (pool.B + 1,), "cu")
     if not isinstance(slot_map, torch.Tensor):
@@ -848,8 +849,9 @@ def kvb_paged_plan(pool, cu, slot_map, workspace, *, empty_only: bool = False, s
         raise TypeError("workspace must be a torch.Tensor")
     _is(workspace, _U8, workspace.shape, "workspace")
     dev = _one_device(cu, slot_map, workspace, *tensors)
-    _launch(dev, stream, "kvb_paged_plan", _lib.lib().kvb_paged_plan, _pool_bytes(pool, tensors), cu.data_ptr(),
-            slot_map.shape[1], slot_map.data_ptr(), 1 if empty_only else 0, workspace.data_ptr(), workspace.numel())
+    _launch(dev, stream, "kvb_paged_plan", _lib.lib().kvb_paged_plan_within, _pool_bytes(pool, tensors), cu.data_ptr(),
+            slot_map.shape[1], slot_map.data_ptr(), 1 if empty_only else 0, min(max_len, 2**31 - 1), workspace.data_ptr(),
+            workspace.numel())
 
 
 def kvb_paged_write(pool, k, v, log_beta, pos, slot_map, *, stream=None) -> None:

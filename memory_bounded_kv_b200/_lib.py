@@ -24,7 +24,7 @@ EXPORTS = (
     "kvb_paged_reset", "kvb_paged_evict_insert", "kvb_paged_decode_attn", "kvb_paged_compact_blocks",
     "kvb_asm_planes_bytes", "kvb_asm_prepare", "kvb_asm_lookup_merge_planes",
     "kvb_prefill_attn", "kvb_prefill_attn_bwd_workspace_bytes", "kvb_prefill_attn_bwd",
-    "kvb_paged_plan_workspace_bytes", "kvb_paged_plan", "kvb_paged_write",
+    "kvb_paged_plan_workspace_bytes", "kvb_paged_plan", "kvb_paged_plan_within", "kvb_paged_write",
 )
 
 KVB_OK, KVB_EINVAL, KVB_ECUDA, KVB_EDEVICE = 0, 1, 2, 3
@@ -147,6 +147,7 @@ def lib() -> ctypes.CDLL:
         L.kvb_paged_plan_workspace_bytes.argtypes = [_I32, _I32]
         L.kvb_paged_plan_workspace_bytes.restype = _SZ
         L.kvb_paged_plan.argtypes = [_P, _P, _I32, _P, _I32, _P, _SZ, _P]
+        L.kvb_paged_plan_within.argtypes = [_P, _P, _I32, _P, _I32, _I32, _P, _SZ, _P]
         L.kvb_paged_write.argtypes = [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I32, _P]
         for f in ("kvb_decode_attn", "kvb_decode_attn_noalloc", "kvb_decode_step", "kvb_merge_states", "kvb_evict_insert", "kvb_compact_blocks",
                   "kvb_asm_lookup_merge", "kvb_asm_hier_lookup_merge", "kvb_asm_aggregate",
@@ -155,7 +156,7 @@ def lib() -> ctypes.CDLL:
                   "kvb_abi_version", "kvb_test_withhold_next_decode", "kvb_test_withhold_next_prefill", "kvb_paged_reset",
                   "kvb_paged_evict_insert", "kvb_paged_decode_attn", "kvb_paged_compact_blocks",
                   "kvb_asm_prepare", "kvb_asm_lookup_merge_planes", "kvb_prefill_attn",
-                  "kvb_prefill_attn_bwd", "kvb_paged_plan", "kvb_paged_write"):
+                  "kvb_prefill_attn_bwd", "kvb_paged_plan", "kvb_paged_plan_within", "kvb_paged_write"):
             getattr(L, f).restype = _I32
         _lib = L
     return _lib

@@ -172,10 +172,10 @@ class PagedKVCache:
         (kvb_prefill_attn, into o and lse) and enter the cache (kvb_paged_plan, kvb_paged_write).
         The attention is that of the decode steps (scores without a cap, scale 1/sqrt(d)) where pos
         rises by one from token to token.
-        A sequence with new tokens must hold none yet; one without keeps what it holds. The pages
-        must have room for the whole prompts; the budget M is enforced by the insertions that
-        follow, each of which replaces a slot of a sequence that holds M or more. kvb_get_error
-        tells of sequences that were not served (their o is written all the same)."""
+        A sequence with new tokens must hold none yet; one without keeps what it holds. A prompt of
+        more than M tokens is not served (KVB_DERR_LEN): the insertions that follow replace slots,
+        so the cache would stay above its budget for good. kvb_get_error tells of sequences that
+        were not served (their o is written all the same)."""
         from . import kvb_paged_plan, kvb_paged_plan_workspace_bytes, kvb_paged_write, kvb_prefill_attn
         # what the write below checks, before anything changes the cache
         T = int(q.shape[0])
@@ -199,7 +199,7 @@ class PagedKVCache:
             workspace = torch.empty(kvb_paged_plan_workspace_bytes(self.B, self.Hkv), dtype=torch.uint8,
                                     device=self.pool.len.device)
             kvb_prefill_attn(q, k, v, lb, cu, o, lse, prefix_len=prefix_len, stream=stream)
-            kvb_paged_plan(self.pool, cu, slot_map, workspace, empty_only=True, stream=stream)
+            kvb_paged_plan(self.pool, cu, slot_map, workspace, empty_only=True, max_len=self.M, stream=stream)
             kvb_paged_write(self.pool, k, v, lb, pos, slot_map, stream=stream)
         self.cand_valid = False
 

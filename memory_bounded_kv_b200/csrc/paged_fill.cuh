@@ -12,6 +12,7 @@ struct PagedPlanParams {
     const int* cu;       // [B + 1]
     int* slot_map;       // [Hkv, T]
     int B, T, empty_only;
+    int most;            // slots that a sequence may hold with its new tokens
     int4* rec;           // workspace [B * Hkv + 1]: old length, new tokens, pages taken by the rows ahead,
                          // served; the last one: the free stack's height before the call, cu in order
 };
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
     griddep_launch_dependents();
     const PagedCache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cap = c.max_pages * kPageSlots;
+    const int cap = c.max_pages * kPageSlots, most = min(cap, p.most);
     const int avail = min(max(*c.free_count, 0), c.num_pages);
     const size_t rows = (size_t)p.B * c.Hkv;
     bool bad = false;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int g = 0; g < 8; ++g) {
                     if (g0 + g >= c.Hkv) continue;
-                    ok = ok && n[g] >= 0 && n[g] <= cap && fresh <= cap - n[g] && !(p.empty_only && n[g] > 0 && fresh > 0);
+                    ok = ok && n[g] >= 0 && n[g] <= cap && (fresh == 0 || (fresh <= most - n[g] && !(p.empty_only && n[g] > 0)));
                     if (ok) need = min(need + pages_of(n[g] + fresh) - pages_of(n[g]), 1 << 30);
                 }
             }

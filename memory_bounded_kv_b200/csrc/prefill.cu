@@ -194,11 +194,17 @@ size_t kvb_paged_plan_workspace_bytes(int32_t B, int32_t Hkv) {
 
 kvb_status kvb_paged_plan(const kvb_paged_cache* c, const int32_t* cu, int32_t T, int32_t* slot_map, int32_t empty_only,
                           void* workspace, size_t workspace_bytes, kvb_stream stream) {
+    return kvb_paged_plan_within(c, cu, T, slot_map, empty_only, INT32_MAX, workspace, workspace_bytes, stream);
+}
+
+kvb_status kvb_paged_plan_within(const kvb_paged_cache* c, const int32_t* cu, int32_t T, int32_t* slot_map,
+                                 int32_t empty_only, int32_t max_len, void* workspace, size_t workspace_bytes,
+                                 kvb_stream stream) {
     kvb::PagedCache pc;
     if (paged_view(c, &pc) != KVB_OK) return KVB_EINVAL;
-    if (T < 0 || T > (1 << 30) || !cu || !aligned4(cu) || (T > 0 && !slot_map) || !aligned4(slot_map)) return KVB_EINVAL;
+    if (max_len < 1 || T < 0 || T > (1 << 30) || !cu || !aligned4(cu) || (T > 0 && !slot_map) || !aligned4(slot_map)) return KVB_EINVAL;
     if (!workspace || !aligned16(workspace) || workspace_bytes < kvb_paged_plan_workspace_bytes(c->B, c->Hkv)) return KVB_EINVAL;
-    kvb::PagedPlanParams p{pc, cu, slot_map, c->B, T, empty_only, static_cast<int4*>(workspace)};
+    kvb::PagedPlanParams p{pc, cu, slot_map, c->B, T, empty_only, max_len, static_cast<int4*>(workspace)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // few slots: the second launch costs more than it spreads (200 tokens, 2 heads: 7.2 -> 6.2 us with the caller's
     // two copies; 131072 tokens, 8 heads need it)

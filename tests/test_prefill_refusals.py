@@ -1,4 +1,6 @@
 """Refusals of the prompt path that reach no device, beside those of test_prefill_host.py."""
+import ctypes
+
 import pytest
 import torch
 
@@ -33,6 +35,17 @@ def test_cache_prefill_refuses_positions_on_another_device(cache):
     with pytest.raises(ValueError, match="pos is on meta"):
         cache.prefill(**dict(cache.good, pos=cache.good["pos"].to("meta")))
     assert cache.called == []
+
+
+def test_plan_within_refuses():
+    F = 1 << 20   # a 16-byte aligned non-null value; the host checks never dereference it
+    c = ctypes.byref(_lib.PagedCacheArgs(k_pages=F, v_pages=F, log_beta_pages=None, pos_pages=F, table=F, len=F, free_pages=F,
+                                         free_count=F, B=2, Hkv=2, d=64, max_pages=4, num_pages=16))
+    L = _lib.lib()
+    ws = L.kvb_paged_plan_workspace_bytes(2, 2)
+    for max_len in (0, -1):
+        assert L.kvb_paged_plan_within(c, F, 8, F, 0, max_len, F, ws, None) == _lib.KVB_EINVAL
+    assert L.kvb_paged_plan_within(c, F, 8, F, 0, 5, F, ws - 1, None) == _lib.KVB_EINVAL
 
 
 @pytest.mark.parametrize("kernel,cta,limit", [(-1, 0, 10**6), (3, 0, 10**6), (0, -1, 10**6), (0, 65536, 10**6), (0, 0, 999),
