@@ -52,8 +52,8 @@ def gradients(q, k, v, log_beta, cu, d_o, d_lse=None, prefix=None, softcap=0.0, 
     """{name: (gradient, bound on its error)}; rows of no document are NaN. For each pair, with B = sum_c |d_o_c v_c|
     and D its row's mean of B plus |d_lse|: dS = p (d_o.v - delta) is off by 2 ETA p (B + D) (p, the fp32 sums of
     d_o.v and delta), P and dS enter the products as bf16, and dq, dk and dv are rounded once. dq of a row whose
-    tile of 128 / G tokens sees more than 128 keys takes delta from o as it was stored, whose error (`forward`'s
-    bound) meets |d_o| and then sum_j p k_j (times the cap's slope)."""
+    tile of 128 / G tokens sees more than 128 keys takes delta from o as it was stored, but for a key of weight
+    above 1/2 (to fp32). That delta's error (of o, `forward`'s bound, times |d_o|) meets p |k| of the other keys."""
     T, Hq, d = q.shape
     Hkv = k.shape[1]
     G = Hq // Hkv
@@ -76,10 +76,15 @@ def gradients(q, k, v, log_beta, cu, d_o, d_lse=None, prefix=None, softcap=0.0, 
             ds = p * (dp - ((p * dp).sum(1) - dl)[:, None])
             b = np.abs(do) @ np.abs(vv).T
             eds = 2 * ETA * p * (b + ((p * b).sum(1) + np.abs(dl))[:, None])
-            estimate = np.where(far, (np.abs(do) * o_bound[s:e, h]).sum(1), 0.0)
+            eps = (np.abs(do) * o_bound[s:e, h]).sum(1)[:, None]
+            at = p.argmax(1)[:, None]
+            top = np.where(np.take_along_axis(p, at, 1) > 0.5 + 8 * ETA, np.take_along_axis(p * slope, at, 1), 0.0)
+            top = top * np.abs(kk)[at[:, 0]]
+            estimate = np.where(far[:, None], eps * ((p * slope) @ np.abs(kk) - top)
+                                + 4 * ETA * ((p * b).sum(1) + np.abs(dl))[:, None] * top, 0.0)
             val["dq"][s:e, h] = scale * (ds * slope) @ kk
             e16 = (eds + BF16 * np.abs(ds)) * slope             # dS as it enters the products
-            bnd["dq"][s:e, h] = scale * (e16 @ np.abs(kk) + estimate[:, None] * np.abs((p * slope) @ kk))
+            bnd["dq"][s:e, h] = scale * (e16 @ np.abs(kk) + estimate)
             val["dk"][s:e, g] += scale * (ds * slope).T @ qq
             bnd["dk"][s:e, g] += scale * e16.T @ np.abs(qq)
             val["dv"][s:e, g] += p.T @ do
