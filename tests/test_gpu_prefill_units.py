@@ -8,7 +8,7 @@ import torch
 import memory_bounded_kv_b200 as kvb
 from gpu_util import host
 import prefill_bounds as bounds
-from test_gpu_prefill import f64, forward, make, reference
+from test_gpu_prefill import backward, f64, forward, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,45 @@ def test_a_neighbours_nan_in_v_between_units(d, beta):
         o, _ = forward(c)
         bounds.within(f64(o), want, bound, "o")
     assert kvb.kvb_get_error() == 0 and host(c["cu"])[-1] == cu[-1]
+
+
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("beta", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d", [(16, 16, 128), (16, 8, 64)])
+def test_gradients_of_several_units_a_cta(Hq, Hkv, d, beta, softcap):
+    """Units of one tile and of several in turn, with rows that have one key above half the weight: every value
+    within its bound, and the same bits each time."""
+    cu = starts(LENGTHS, 62 + d)
+    c = make(62, cu, cu[-1], Hq, Hkv, d, beta, grads=True, d_lse=True)
+    if beta:
+        c["lb"][:, ::2] -= 3
+    a = [f64(c[n]) for n in ("q", "k", "v", "lb")]
+    want = bounds.gradients(*a, cu, f64(c["d_o"]), f64(c["d_lse"]), None, softcap)
+    o, lse = forward(c, None, softcap)
+    first = backward(c, o, lse, None, softcap)
+    for n, x in first.items():
+        if x is not None:
+            bounds.within(f64(x), *want[n], n)
+    for _ in range(6):
+        again = backward(c, o, lse, None, softcap)
+        assert all(x is None or torch.equal(x, again[n]) for n, x in first.items())
+    assert kvb.kvb_get_error() == 0
+
+
+@pytest.mark.parametrize("beta", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_neighbours_nan_in_the_gradients_of_several_units(d, beta):
+    """Every second document is NaN throughout: the others' gradients are theirs."""
+    cu = starts(LENGTHS, 63)
+    c = make(63, cu, cu[-1], 16, 8, d, beta, grads=True)
+    want = bounds.gradients(*[f64(c[n]) for n in ("q", "k", "v", "lb")], cu, f64(c["d_o"]))
+    for s, e in list(zip(cu[:-1], cu[1:]))[::2]:
+        for n in ("q", "k", "v", "d_o"):
+            c[n][s:e] = float("nan")
+        for n in want:
+            want[n][0][s:e] = np.nan
+    o, lse = forward(c)
+    for n, x in backward(c, o, lse).items():
+        if x is not None:
+            bounds.within(f64(x), *want[n], n)
+    assert kvb.kvb_get_error() == 0
