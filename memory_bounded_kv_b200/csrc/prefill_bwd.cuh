@@ -206,11 +206,9 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                 }
                 __syncwarp();
                 if (end) break;
-                bool withheld = false;
-                for (int tile = n - 1; tile >= 0; --tile, ++step) {
+                const int loads = p.withhold == blockIdx.x + 1 ? min(n, max(1 - step, 0)) : n;   // test hook: one tile in all
+                for (int tile = n - 1; tile >= n - loads; --tile, ++step) {
                     const int st = step % ST;
-                    withheld = step > 0 && p.withhold == blockIdx.x + 1;
-                    if (withheld) break;
                     if (step >= ST && !warp_wait(&kv_empty[st], (unsigned)((step / ST) - 1) & 1u, p.wait_ns)) { stop = true; break; }
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&kv_full[st], (unsigned)(2 * SH::KTILE));
@@ -223,7 +221,7 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     }
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
-                if (withheld) break;
+                if (loads < n) break;
             }
             if (stop && lane == 0) fail();
         } else if (warp == 10) {
@@ -732,14 +730,17 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REG_REST));
         if (warp == 9) {
             // ======================= units and loads =======================
-            // where a CTA of the kernel by query rows gave up, its deltas are not there: nothing is done
-            bool lost = false;
-            for (int c = lane; c < p.dq_ctas; c += 32) lost |= p.dq_done[c] == 0;
-            lost = __any_sync(kFull, lost);
+            int done = 1;   // its loads go out together, ahead of the walks' own
+            static_assert(kMaxPieces % 32 == 0, "a lane per CTA");
+#pragma unroll
+            for (int c = 0; c < kMaxPieces; c += 32)
+                if (c + lane < p.dq_ctas) done &= p.dq_done[c + lane];
             const StepLine line(p);
             const bool cut = line.cut(gridDim.x);
             const long long piece = line.piece(gridDim.x), x1 = min((blockIdx.x + 1) * piece, line.steps);
             const PrefillWalk walk(p, 7);
+            // where a CTA of the kernel by query rows gave up, its deltas are not there: nothing is done
+            const bool lost = __any_sync(kFull, done == 0);
             int step = 0, uc = 0;
             bool stop = false;
             long long x = blockIdx.x * piece, round = 0;
@@ -804,11 +805,9 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     }
                     s_steps[1] = uc + 1;
                 }
-                bool withheld = false;
-                for (int b = b0; b < b1; ++b, ++step) {
+                const int till = p.withhold == blockIdx.x + 1 ? min(b1, b0 + max(1 - step, 0)) : b1;   // test hook
+                for (int b = b0; b < till; ++b, ++step) {
                     const int st = step % ST;
-                    withheld = step > 0 && p.withhold == blockIdx.x + 1;
-                    if (withheld) break;
                     if (step >= ST && !warp_wait(&q_empty[st], (unsigned)((step / ST) - 1) & 1u, p.wait_ns)) { stop = true; break; }
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&q_full[st], (unsigned)(2 * SH::TILE));
@@ -821,7 +820,7 @@ __global__ void __launch_bounds__(DkvShape<D>::NT, 1)
                     }
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
-                if (stop || withheld) break;
+                if (stop || till < b1) break;
             }
             if (lane == 0) p.records[blockIdx.x] = record;
             if (stop && lane == 0) fail();

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                     break;
                 }
                 const int n = max(n0, n1);
-                bool withheld = false;
+                const int loads = p.withhold == blockIdx.x + 1 ? min(n, max(1 - step, 0)) : n;   // test hook: one tile in all
                 if (lane == 0) {
                     const int tiles = n1 > 0 ? 2 : 1;
                     mbar_arrive_expect_tx(q_full, (unsigned)(tiles * SH::TILE));
@@ -212,11 +212,9 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                                         x.s + (x.blk << sh) + (t << (sh - 1)), q_full);
                     s_steps[1] = uc + 1;
                 }
-                for (int tile = n - 1; tile >= 0; --tile, ++step) {
+                for (int tile = n - 1; tile >= n - loads; --tile, ++step) {
                     const int st = step % ST;
                     const unsigned ph = (unsigned)((step / ST) - 1) & 1u;
-                    withheld = step > 0 && p.withhold == blockIdx.x + 1;
-                    if (withheld) break;
                     if (step >= ST && !warp_wait(&k_empty[st], ph, p.wait_ns)) { stop = true; break; }
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&k_full[st], (unsigned)SH::TILE);
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(FwdShape<D>::NT, 1)
                     if (__any_sync(kFull, *s_abort != 0)) { stop = true; break; }
                 }
                 if (stop && lane == 0) fail();
-                if (withheld) break;
+                if (loads < n) break;
             }
         } else if (warp >= 10) {
             // ======================= bias columns, V past a document's end =======================
