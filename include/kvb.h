@@ -433,10 +433,18 @@ kvb_status kvb_paged_compact_blocks(const kvb_paged_cache* cache, const int32_t*
  * rows of the results that it had not written keep what they held, and so do
  * the rows of dk, dv and d_log_beta whose sum it holds a part of -- all their
  * rows where a CTA of the gradients by query rows gave up (delta is missing).
- * An infinity or a NaN in a row reaches no other document. One in v_j or d_o_i
- * may also reach pairs (i, j) of the same document that do not see each other
- * (their weight is 0, and 0 times it is NaN), as in the formula's products.
- *
+ * An infinity or a NaN in a row reaches no other document. Within its own it
+ * reaches o and lse of the rows that see it; one in v_j may also reach o, and
+ * one in q_i, k_j, v_j or d_o_i the gradients, of pairs (i, j) that do not see
+ * each other (their weight is 0, and 0 times it is NaN), as in the formula's
+ * products.
+ * Precision: scores, bias, softmax statistics, delta, d_log_beta and all sums
+ * are fp32. The weights p enter P V, and p and ds the gradients' products, as
+ * bf16 (2^-8 of each), and o, dq, dk and dv are rounded once more. dq of a row
+ * past the first 128 keys of its document takes delta from o as it was stored,
+ * but for a key of p above 1/2: it may be off by scale eps_i sum p_ij |k_j|
+ * over the other keys, eps_i <= 2^-7 sum_c |d_o_ic| sum_j p_ij |v_jc|. At
+ * d = 64 a quarter of the exponentials is a polynomial (forward 2.6e-6).
  * Requirements: d in {64, 128}; Hq / Hkv in {1, 2, 4, 8}; T <=
  * KVB_PREFILL_MAX_TOKENS (distances are exact in fp32), N <=
  * KVB_PREFILL_MAX_DOCS; q, k, v, o and the bf16 gradients 16-byte aligned;
