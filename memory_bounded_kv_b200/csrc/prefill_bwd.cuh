@@ -14,7 +14,7 @@
 // than the rounding of dS to bf16; where one key has almost all, dS_ij = p_ij (dP_ij - delta_i) is small and eps_i
 // is not. So a key of weight above 1/2 (a row has one at most) is kept, and eps_i p_ij k_j is taken from dq_i.
 // Log beta of -3 to -5, 1000 tokens, 8/2 heads: dq off by 4 % in the middle row and 1.3 % in all -> 0.25 % each,
-// for 0.5 % of the time on a document of 8192 tokens and 3 % on documents of 250. Rows whose keys fit one tile
+// for 3 % of the time on documents of 250 tokens and next to none on one of 8192. Rows whose keys fit one tile
 // take delta itself at once.
 //
 // What bounds both is shared memory and the hand-over between products and softmax. A product of two
@@ -469,6 +469,20 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     x[c] = u;
                     x[c + 1] = v;
                 }
+                float most[2] = {0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 64; c += 4) {
+                    most[0] = max3(most[0], x[c], x[c + 1]);
+                    most[1] = max3(most[1], x[c + 2], x[c + 3]);
+                }
+                if (__any_sync(kFull, fmaxf(most[0], most[1]) > 0.5f)) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (x[c] > 0.5f) {
+                            top = x[c] * (CAP ? fmaf(th[c] * th[c], inv_cap2, 1.f) : 1.f);
+                            top_j = j0 + c;
+                        }
+                }
                 uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
                 if (!warp_wait(dp_full, (unsigned)step & 1u, p.wait_ns)) { stop = true; break; }
                 tc_fence_after();
@@ -501,17 +515,6 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     float dp[32];
                     tmem_ld32(tl + SH::TM_DP + t * 64 + c0, dp);
                     tmem_ld_wait();
-                    float most = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) most = max3(most, x[c0 + e], x[c0 + e + 1]);
-                    if (__any_sync(kFull, most > 0.5f)) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (x[c0 + e] > 0.5f) {
-                                top = x[c0 + e] * (CAP ? fmaf(th[c0 + e] * th[c0 + e], inv_cap2, 1.f) : 1.f);
-                                top_j = j0 + c0 + e;
-                            }
-                    }
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
