@@ -31,8 +31,9 @@
 // adds up the few that a cut goes through.
 //   The two warpgroups share a tile: each takes 64 of its 128 columns, a thread per row.
 // The bias rides the S product as in prefill_fwd_kernel; by keys, - lse and - delta ride S and dP too.
-// One document of 8192 tokens, 32/8 heads, d 128: by query rows 690 us (3 products, 1.2 PFLOP/s), by keys
-// 890 us (4 products, 1.24 PFLOP/s), both near the power cap in long runs; d 64 560 and 630 us.
+// One document of 8192 tokens, 32/8 heads, d 128: by query rows 725 us (3 products, 1.14 PFLOP/s), by keys
+// 925 us (4 products, 1.19 PFLOP/s), both near the power cap in long runs; d 64 627 and 617 us; d 128 with a cap
+// of 50 1155 and 1250 us.
 #pragma once
 
 #include "prefill_units.cuh"
@@ -469,13 +470,10 @@ __global__ void __launch_bounds__(DqShape<D>::NT, 1)
                     x[c] = u;
                     x[c + 1] = v;
                 }
-                float most[2] = {0.f, 0.f};
+                float most[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < 64; c += 4) {
-                    most[0] = max3(most[0], x[c], x[c + 1]);
-                    most[1] = max3(most[1], x[c + 2], x[c + 3]);
-                }
-                if (__any_sync(kFull, fmaxf(most[0], most[1]) > 0.5f)) {
+                for (int c = 0; c < 64; c += 2) most[(c / 2) & 3] = max3(most[(c / 2) & 3], x[c], x[c + 1]);
+                if (__any_sync(kFull, max3(most[0], most[1], fmaxf(most[2], most[3])) > 0.5f)) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c)
                         if (x[c] > 0.5f) {

@@ -28,7 +28,7 @@
 // and takes some 3400, the rest being the hand-over between products and softmax: a tile's next S waits
 // for its P V, because two S and two O fill the tensor memory. One document of 8192 tokens, 32/8 heads,
 // d 128: 435 us (1.26 PFLOP/s) in short bursts, 501 us at the power cap; d 64 368 us (exponentials); with
-// capped scores 800 us. Short documents pay a near tile and 2.5k clocks of output a unit: 6151 tokens in
+// scores capped at 50 765 us. Short documents pay a near tile and 2.5k clocks of output a unit: 6151 tokens in
 // 24 documents 59 us. One issuing warp, not one per tile: with two, both tiles' products interleave and
 // both finish late (475 -> 537 us). Pairs always: a tile alone takes 0.83 of a pair's step, so units of
 // one tile lose even where the longest pair holds up the rest (4000 tokens in 5 documents, 16/2 heads, d 64,
