@@ -67,3 +67,21 @@ def test_plan_within(held, new, max_len, empty_only):
         np.testing.assert_array_equal(host(got), w)
     assert int(pool.free_count) == want[3]
     assert bool(bits & _lib.DERR_LEN) == (any(past) or "len" in want[4]) and not bits & ~_lib.DERR_LEN
+
+
+def test_plan_of_few_tokens_among_many_sequences():
+    """The one-launch form with more sequences than its block has threads."""
+    B, H, width, pages = 2100, 2, 2, 9000
+    g = np.random.default_rng(93)
+    held = g.integers(0, 65, B).tolist()
+    new = np.where(g.random(B) < 0.3, g.integers(1, 4, B), 0)
+    pool = filled_pool(93, B, H, width, pages, held)
+    cu = np.r_[3, 3 + np.cumsum(new)].astype(np.int32)
+    slot_map = torch.full((H, int(cu[-1]) + 1), -7, dtype=torch.int32, device="cuda")
+    assert slot_map.numel() <= 4096
+    want = ref.plan(cu, host(pool.len), host(pool.table), host(pool.free_pages), int(pool.free_count), host(slot_map), pages, PAGE)
+    ws = torch.empty(kvb.kvb_paged_plan_workspace_bytes(B, H), dtype=torch.uint8, device="cuda")
+    kvb.kvb_paged_plan(pool, torch.from_numpy(cu).cuda(), slot_map, ws)
+    for got, w in ((slot_map, want[0]), (pool.table, want[1]), (pool.len, want[2])):
+        np.testing.assert_array_equal(host(got), w)
+    assert int(pool.free_count) == want[3] and kvb.kvb_get_error() == 0
